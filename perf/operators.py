@@ -41,8 +41,8 @@ def _quantize(name, batch, rows, cols, block_rows, src):
     return dict(c, name=name) if name else c
 
 
-def _gemm(name, T, d, E, k, N):
-    c = {"op": "gemm", "T": T, "d": d, "E": E, "k": k, "F": N, "padded": 0.0}
+def _gemm(name, T, d, E, k, N, out="bf16"):
+    c = {"op": "gemm", "T": T, "d": d, "E": E, "k": k, "F": N, "padded": 0.0, "out": out}
     return dict(c, name=name) if name else c
 
 
@@ -64,7 +64,7 @@ def listed():
         # a layer's expert matrices when the weights are loaded
         _quantize("quantize_weights_128", 128, 768, 2048, 128, "bf16"),
         # one projection of an expert layer for a ragged decode batch
-        _gemm("gemm_33_tokens", 33, 2048, 64, 8, 1024),
+        _gemm("gemm_33_tokens", 33, 2048, 64, 8, 1024, "f32"),
         # a dense layer (one expert that every token takes) in prefill
         _gemm("gemm_2000_dense", 2000, 4096, 1, 1, 4096),
         # decode of one request
@@ -105,8 +105,10 @@ def draw(rng):
     E = rng.choice([8, 16, 60, 64, 128])
     if op == "gemm":
         if rng.random() < 0.3:
-            return _gemm(None, _log(rng, 1, 2000), 16 * _log(rng, 8, 256), 1, 1, 16 * _log(rng, 8, 256))
-        return _gemm(None, _log(rng, 1, 1000), 16 * _log(rng, 8, 128), E, rng.randint(1, 8), 16 * _log(rng, 8, 64))
+            return _gemm(None, _log(rng, 1, 2000), 16 * _log(rng, 8, 256), 1, 1, 16 * _log(rng, 8, 256),
+                         rng.choice(["bf16", "f32"]))
+        return _gemm(None, _log(rng, 1, 1000), 16 * _log(rng, 8, 128), E, rng.randint(1, 8), 16 * _log(rng, 8, 64),
+                     rng.choice(["bf16", "f32"]))
     return _ffn(None, _log(rng, 1, 3000), 16 * _log(rng, 16, 128), E, rng.randint(1, 8), 16 * _log(rng, 8, 64),
                 rng.choice([0.0, 0.0, 0.2]), rng.choice(["bf16", "f32"]))
 
@@ -291,7 +293,7 @@ def _gemm_plain(state):
     xe, active, slot, rank, real = _by_expert(x, state)
     q, scale = state["W"]
     y = torch.bmm(xe, _dequantized(q[active], scale[active]).transpose(1, 2))[slot, rank]
-    return torch.where(real[:, None], y, torch.zeros((), device="cuda")).to(torch.bfloat16)
+    return torch.where(real[:, None], y, torch.zeros((), device="cuda")).to(TYPES[state["case"]["out"]])
 
 
 def _dequantized_rows(q, scale):
@@ -340,7 +342,7 @@ def _run_own(state):
                        else moe.new_blocks_workspace(c["T"], c["d"], c["E"], c["k"], c["F"]))
     if c["op"] == "gemm":
         if "y" not in state:  # rows past the last list entry stay as they are
-            state["y"] = torch.zeros(c["T"] * c["k"], c["F"], dtype=torch.bfloat16, device="cuda")
+            state["y"] = torch.zeros(c["T"] * c["k"], c["F"], dtype=TYPES[c["out"]], device="cuda")
         return {"y": moe.moe_expert_gemm_blocks(state["q"], state["scale"], *state["W"], state["lists"], c["k"],
                                                 ws=state["ws"], y=state["y"])}
     return {"y": moe.moe_expert_ffn_blocks(state["x"], *state["W"], state["lists"], c["k"], ws=state["ws"],
@@ -376,7 +378,7 @@ def work(case):
     n_active = int(torch.unique(e[e >= 0]).numel())
     scales = -(-d // BLOCK) * -(-F // BLOCK) * 4
     if op == "gemm":
-        return {"bytes": n_active * (d * F + scales) + T * (d + 4 * -(-d // BLOCK)) + pairs * F * 2,
+        return {"bytes": n_active * (d * F + scales) + T * (d + 4 * -(-d // BLOCK)) + pairs * F * (2 if case["out"] == "bf16" else 4),
                 "flops": 2 * pairs * d * F}
     return {"bytes": n_active * 3 * (d * F + scales) + T * d * ((2 if case["src"] == "bf16" else 4) + 2) + pairs * 8,
             "flops": 6 * pairs * d * F}
