@@ -8,7 +8,10 @@ built for this machine, importing the binding's functions raises.
 
 Entry points mirror the C ABI in include/moe_decode.h:
 ``moe_route``, ``moe_reselect``, ``moe_expert_ffn``, ``moe_layer_decode``,
-``moe_workspace_bytes``, ``moe_check_error``, ``moe_status_string``.
+``moe_workspace_bytes``, ``moe_check_error``, ``moe_status_string``; the
+general router ``moe_route_scored``; the block-scaled 8-bit operators
+``moe_quantize_blocks``, ``moe_expert_gemm_blocks`` and
+``moe_expert_ffn_blocks``.
 """
 from __future__ import annotations
 
@@ -25,6 +28,9 @@ __all__ = [
     "moe_check_error", "moe_expert_ffn_noalloc", "new_workspace", "alloc_lists", "ABI_SYMBOLS",
     "NOALLOC_SCRATCH_BYTES", "moe_set_wait_limit_ns", "moe_decode_stack", "LayerWeights",
     "MOE_PHASE_DECODE", "MOE_PHASE_PREFILL", "moe_down_channel_major", "moe_expert_ffn_channels",
+    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "Scoring", "BlockWeights", "moe_route_scored", "new_route_workspace",
+    "moe_quantize_blocks", "moe_expert_gemm_blocks", "new_gemm_workspace", "moe_expert_ffn_blocks",
+    "new_blocks_workspace", "GEMM_WORKSPACE_BYTES",
 ]
 
 MOE_RESELECT_NONE, MOE_RESELECT_OEA, MOE_RESELECT_XSHARE = 0, 1, 2
@@ -34,8 +40,13 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_MISALIGNED", 3: "MO
 ABI_SYMBOLS = ("moe_workspace_bytes", "moe_route", "moe_reselect", "moe_expert_ffn",
                "moe_layer_decode", "moe_expert_ffn_noalloc", "moe_check_error", "moe_status_string",
                "moe_set_wait_limit_ns", "moe_decode_stack", "moe_down_channel_major",
-               "moe_channels_workspace_bytes", "moe_expert_ffn_channels")
+               "moe_channels_workspace_bytes", "moe_expert_ffn_channels", "moe_route_workspace_bytes",
+               "moe_route_scored", "moe_quantize_blocks", "moe_expert_gemm_blocks", "moe_blocks_workspace_bytes",
+               "moe_expert_ffn_blocks")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+GEMM_WORKSPACE_BYTES = 4096
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype_t
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe_decode.so")
@@ -66,6 +77,16 @@ class LayerWeights(ctypes.Structure):
 class Lists(ctypes.Structure):
     _fields_ = [("n_active", ctypes.c_void_p), ("active", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("tok", ctypes.c_void_p), ("w", ctypes.c_void_p)]
+
+
+class Scoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class BlockWeights(ctypes.Structure):
+    _fields_ = [("Wgate", ctypes.c_void_p), ("Sgate", ctypes.c_void_p), ("Wup", ctypes.c_void_p),
+                ("Sup", ctypes.c_void_p), ("Wdown", ctypes.c_void_p), ("Sdown", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -105,6 +126,19 @@ def load_library() -> ctypes.CDLL:
         lib.moe_channels_workspace_bytes.argtypes = [Dims]
         lib.moe_expert_ffn_channels.restype = ctypes.c_int
         lib.moe_expert_ffn_channels.argtypes = [P, P, P, P, Dims, P, P, P, ctypes.c_int32, P, P, P, S, P]
+        lib.moe_route_workspace_bytes.restype = S
+        lib.moe_route_workspace_bytes.argtypes = [Dims]
+        lib.moe_route_scored.restype = ctypes.c_int
+        lib.moe_route_scored.argtypes = [P, P, Dims, Scoring, P, P, Lists, P, S, P]
+        lib.moe_quantize_blocks.restype = ctypes.c_int
+        lib.moe_quantize_blocks.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int32, P, P, P]
+        lib.moe_expert_gemm_blocks.restype = ctypes.c_int
+        lib.moe_expert_gemm_blocks.argtypes = [P, P, P, P, Dims, Lists, P, ctypes.c_int32, P, S, P]
+        lib.moe_blocks_workspace_bytes.restype = S
+        lib.moe_blocks_workspace_bytes.argtypes = [Dims]
+        lib.moe_expert_ffn_blocks.restype = ctypes.c_int
+        lib.moe_expert_ffn_blocks.argtypes = [P, ctypes.c_int32, BlockWeights, Dims, Lists, P, ctypes.c_int32, P, S, P]
         lib.moe_set_wait_limit_ns.restype = None
         lib.moe_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
         _lib = lib
@@ -286,6 +320,114 @@ def moe_expert_ffn_channels(x, Wgate, Wup, WdownT, sel_idx, sel_w, score, c: int
                                      _ptr(sel_w), _ptr(score), int(c), _ptr(y), _ptr(keep), _ptr(ws),
                                      ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "moe_expert_ffn_channels")
+    return y
+
+
+def _dtype(t) -> int:
+    code = _DTYPES.get(t if isinstance(t, torch.dtype) else t.dtype)
+    if code is None:
+        raise TypeError("expected a float32 or bfloat16 tensor")
+    return code
+
+
+def _bytes(ws) -> int:
+    return ws.numel() * ws.element_size()
+
+
+def _new_bytes(n: int, where: str, device) -> torch.Tensor:
+    if n == 0:
+        raise MoeError(1, where)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def new_route_workspace(B: int, E: int, k: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_route_scored."""
+    n = int(load_library().moe_route_workspace_bytes(Dims(B, 0, E, k, 0)))
+    return _new_bytes(n, "moe_route_workspace_bytes", device)
+
+
+def new_gemm_workspace(device="cuda") -> torch.Tensor:
+    """Workspace of moe_expert_gemm_blocks."""
+    return torch.zeros(GEMM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def new_blocks_workspace(B: int, d: int, E: int, k: int, d_ff: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_expert_ffn_blocks."""
+    n = int(load_library().moe_blocks_workspace_bytes(Dims(B, d, E, k, d_ff)))
+    return _new_bytes(n, "moe_blocks_workspace_bytes", device)
+
+
+def moe_route_scored(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
+                     group_best: int = 1, renorm: bool = True, scale: float = 1.0, out=None, lists=None, ws=None,
+                     stream=None):
+    """-> (sel_idx[B][k], sel_w[B][k], lists dict) from router logits[B][E]
+    fp32: softmax or sigmoid scores, a bias that steers the choice, expert
+    groups, top-k, weights."""
+    B, E = logits.shape
+    if out is None:
+        out = (torch.empty(B, k, dtype=torch.int32, device=logits.device),
+               torch.empty(B, k, dtype=torch.float32, device=logits.device))
+    if lists is None:
+        lists = alloc_lists(B, E, k, logits.device)
+    if ws is None:
+        ws = new_route_workspace(B, E, k, logits.device)
+    sel, w = out
+    st = load_library().moe_route_scored(_ptr(logits), _ptr(bias), Dims(B, 0, E, k, 0),
+                                         Scoring(score, groups, top_groups, group_best, int(renorm), scale),
+                                         _ptr(sel), _ptr(w), _lists(lists), _ptr(ws), _bytes(ws), _stream(stream))
+    _check(st, "moe_route_scored")
+    return sel, w, lists
+
+
+def moe_quantize_blocks(x, block_rows: int = 1, q=None, scale=None, stream=None):
+    """-> (q e4m3, scale fp32) of x[..., rows, cols] (fp32 or bf16): a
+    power-of-two scale per 128 columns of a row (block_rows 1: scale[...,
+    rows, ceil(cols / 128)]) or per 128 x 128 block (block_rows 128)."""
+    rows, cols = x.shape[-2:]
+    batch = x.numel() // (rows * cols) if rows * cols else 0
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        rb = rows if block_rows == 1 else -(-rows // 128)
+        scale = torch.empty(*x.shape[:-2], rb, -(-cols // 128), dtype=torch.float32, device=x.device)
+    st = load_library().moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows, _ptr(q), _ptr(scale),
+                                            _stream(stream))
+    _check(st, "moe_quantize_blocks")
+    return q, scale
+
+
+def moe_expert_gemm_blocks(q, scale, W, Wscale, lists: dict, k: int, ws=None, y=None, y_dtype=torch.bfloat16,
+                           stream=None):
+    """-> y[B * k][rows] = W[e] x of every list entry; q[B][d] e4m3 with
+    scale[B][ceil(d / 128)], W[E][rows][d] e4m3 with Wscale[E][ceil(rows /
+    128)][ceil(d / 128)].  Rows past the last list entry keep what y held."""
+    B, d = q.shape
+    E, F, _ = W.shape
+    if ws is None:
+        ws = new_gemm_workspace(q.device)
+    if y is None:
+        y = torch.empty(B * k, F, dtype=y_dtype, device=q.device)
+    st = load_library().moe_expert_gemm_blocks(_ptr(q), _ptr(scale), _ptr(W), _ptr(Wscale), Dims(B, d, E, k, F),
+                                               _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws),
+                                               _stream(stream))
+    _check(st, "moe_expert_gemm_blocks")
+    return y
+
+
+def moe_expert_ffn_blocks(x, Wgate, Sgate, Wup, Sup, Wdown, Sdown, lists: dict, k: int, ws=None, y=None,
+                          y_dtype=None, stream=None):
+    """-> y[B][d] (y_dtype: fp32 or bf16, x's type by default): the expert
+    FFN of moe_expert_ffn on block-scaled e4m3 weights; x fp32 or bf16."""
+    B, d = x.shape
+    E, F, _ = Wgate.shape
+    if ws is None:
+        ws = new_blocks_workspace(B, d, E, k, F, x.device)
+    if y is None:
+        y = torch.empty(B, d, dtype=y_dtype or x.dtype, device=x.device)
+    st = load_library().moe_expert_ffn_blocks(
+        _ptr(x), _dtype(x), BlockWeights(_ptr(Wgate), _ptr(Sgate), _ptr(Wup), _ptr(Sup), _ptr(Wdown), _ptr(Sdown)),
+        Dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws), _stream(stream))
+    _check(st, "moe_expert_ffn_blocks")
     return y
 
 

@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_decode.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["router.cu", "expert.cu", "abi.cu", "noalloc.cu", "channels.cu"]
+SOURCES = ["router.cu", "expert.cu", "abi.cu", "noalloc.cu", "channels.cu", "route_scored.cu",
+           "quant.cu", "blocks.cu"]
 GENCODE = "arch=compute_100a,code=sm_100a"
 
 

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "blocks.h"
 #include "internal.h"
 
 namespace moe {
@@ -46,6 +47,25 @@ bool rule_ok(const moe_dims_t &d, const moe_reselect_t &r) {
         default: return false;
     }
 }
+
+// Limits of the scored router (B, E, k) and of the block-scaled operators.
+bool dims_ok_scored(const moe_dims_t &d) {
+    return d.B >= 1 && d.B <= ST_MAX && d.k >= 1 && d.k <= K_MAX && d.E >= d.k && d.E <= SE_MAX;
+}
+bool dims_ok_blocks(const moe_dims_t &d) {
+    return dims_ok_scored(d) && d.d >= SD_MIN && d.d <= SD_MAX && d.d % 16 == 0 && d.d_ff >= SD_MIN &&
+           d.d_ff <= SD_MAX && d.d_ff % 16 == 0;
+}
+
+bool scoring_ok(const moe_dims_t &d, const moe_scoring_t &r) {
+    if (r.score != MOE_SCORE_SOFTMAX && r.score != MOE_SCORE_SIGMOID) return false;
+    if (r.groups < 1 || r.groups > 32 || d.E % r.groups != 0) return false;
+    if (r.top_groups < 1 || r.top_groups > r.groups || r.group_best < 1 || r.group_best > 2) return false;
+    if (r.renorm != 0 && r.renorm != 1) return false;
+    return r.scale > 0.0f && r.scale <= 3.0e38f;
+}
+
+bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool al256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
@@ -233,11 +253,53 @@ bool encode_expert_maps(ExpertMaps *m, const moe_dims_t &d, const uint16_t *Wgat
                                       gu_chunks));
 }
 
+bool encode_product_maps(ProductMaps *m, const void *a, uint64_t a_rows, const void *b0, const void *b1,
+                         uint64_t E, uint64_t rows, uint64_t K) {
+    std::memset(m, 0, sizeof(*m));
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint32_t one[3] = {1, 1, 1};
+    // activation rows: boxes of one row, gathered four at a time
+    cuuint64_t adim[2] = {K, a_rows}, astride[1] = {K};
+    cuuint32_t abox[2] = {BLK, 1};
+    if (fn(&m->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(a), adim, astride, abox, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    // weights: boxes of 128 rows x 128 bytes; rows and columns past the end
+    // of a matrix read as zero
+    cuuint64_t bdim[3] = {K, rows, E}, bstride[2] = {K, rows * K};
+    cuuint32_t bbox[3] = {BLK, BLK, 1};
+    const void *b[2] = {b0, b1};
+    CUtensorMap *out[2] = {&m->b0, &m->b1};
+    for (int i = 0; i < 2; ++i)
+        if (fn(out[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(b[i]), bdim, bstride, bbox, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
 bool encode_router_maps(RouterMaps *m, const moe_dims_t &d, const float *x, const float *Wg) {
     std::memset(m, 0, sizeof(*m));
     const uint32_t bl = static_cast<uint32_t>(router_box_lines(d.d));
     return encode_f32_lines(&m->x, x, static_cast<uint64_t>(d.B), static_cast<uint64_t>(d.d), bl) &&
            encode_f32_lines(&m->wg, Wg, static_cast<uint64_t>(d.E), static_cast<uint64_t>(d.d), bl);
+}
+
+BlocksWs blocks_ws(const moe_dims_t &d) {
+    BlocksWs w;
+    const size_t B = d.B, k = d.k, D = d.d, F = d.d_ff, P = B * k;
+    size_t o = MOE_GEMM_WORKSPACE_BYTES;
+    w.xq = o;  o += round_up(B * D);
+    w.xs = o;  o += round_up(B * blocks_of(d.d) * 4);
+    w.hq = o;  o += round_up(P * F);
+    w.hs = o;  o += round_up(P * blocks_of(d.d_ff) * 4);
+    w.yp = o;  o += round_up(P * D * 4);
+    w.cnt = o; o += round_up(B * 4);
+    w.inv = o; o += round_up(P * 4);
+    w.total = o;
+    return w;
 }
 
 unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
@@ -466,6 +528,139 @@ moe_status_t moe_expert_ffn_channels(const float *x, const uint16_t *Wgate, cons
     if (st != MOE_OK) return st;
     return from_cuda(launch_channels(x, Wgate, Wup, WdownT, dims, sel_idx, sel_w, score, c, y, keep, ws,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_route_workspace_bytes(moe_dims_t dims) { return dims_ok_scored(dims) ? route_ws_bytes(dims) : 0; }
+
+moe_status_t moe_route_scored(const float *logits, const float *bias, moe_dims_t dims, moe_scoring_t rule,
+                              int32_t *sel_idx, float *sel_w, moe_lists_t lists, void *ws, size_t ws_bytes,
+                              void *stream) {
+    if (!dims_ok_scored(dims) || !scoring_ok(dims, rule)) return MOE_ERR_INVALID_ARG;
+    if (!logits || !sel_idx || !sel_w) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_lists(lists);
+    if (st != MOE_OK) return st;
+    if (!al16(logits) || (bias && !al16(bias)) || !al16(sel_idx) || !al16(sel_w)) return MOE_ERR_MISALIGNED;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    if (!al256(ws)) return MOE_ERR_MISALIGNED;
+    if (ws_bytes < route_ws_bytes(dims)) return MOE_ERR_WORKSPACE;
+    st = check_device();
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_route_scored(logits, bias, dims, rule, sel_idx, sel_w, lists, ws,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_quantize_blocks(const void *x, int32_t type, int64_t batch, int64_t rows, int64_t cols,
+                                 int32_t block_rows, uint8_t *q, float *scale, void *stream) {
+    if (!x || !q || !scale || !dtype_ok(type) || (block_rows != 1 && block_rows != BLK)) return MOE_ERR_INVALID_ARG;
+    if (batch < 1 || rows < 1 || batch > INT32_MAX || rows > INT32_MAX || batch * rows > INT32_MAX ||
+        cols < SD_MIN || cols > 4 * SD_MAX || cols % 16 != 0)
+        return MOE_ERR_INVALID_ARG;
+    const int64_t row_blocks = block_rows == 1 ? rows : (rows + BLK - 1) / BLK;
+    if (batch * row_blocks * blocks_of(static_cast<int>(cols)) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (!al16(x) || !al16(q) || !al16(scale)) return MOE_ERR_MISALIGNED;
+    const moe_status_t st = check_device();
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_quantize(x, type, batch, rows, cols, block_rows, q, scale, nullptr, 0,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const uint8_t *W, const float *Wscale,
+                                    moe_dims_t dims, moe_lists_t lists, void *y, int32_t y_type, void *ws,
+                                    size_t ws_bytes, void *stream) {
+    if (!dims_ok_blocks(dims) || !dtype_ok(y_type)) return MOE_ERR_INVALID_ARG;
+    if (!q || !scale || !W || !Wscale || !y) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_lists(lists);
+    if (st != MOE_OK) return st;
+    if (!al16(q) || !al16(scale) || !al16(W) || !al16(Wscale) || !al16(y)) return MOE_ERR_MISALIGNED;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    if (!al256(ws)) return MOE_ERR_MISALIGNED;
+    if (ws_bytes < MOE_GEMM_WORKSPACE_BYTES) return MOE_ERR_WORKSPACE;
+    st = check_device();
+    if (st != MOE_OK) return st;
+    ProductMaps maps;
+    if (!encode_product_maps(&maps, q, dims.B, W, W, dims.E, dims.d_ff, dims.d)) return MOE_ERR_CUDA;
+    ProductArgs a = {};
+    a.kind = PRODUCT_OUT;
+    a.B = dims.B;
+    a.E = dims.E;
+    a.k = dims.k;
+    a.K = dims.d;
+    a.rows = dims.d_ff;
+    a.as = scale;
+    a.bs0 = a.bs1 = Wscale;
+    a.n_active = lists.n_active;
+    a.active = lists.active;
+    a.offsets = lists.offsets;
+    a.tok = lists.tok;
+    a.out = y;
+    a.out_bf16 = y_type == MOE_BF16;
+    a.error = &static_cast<BlocksControl *>(ws)->error;
+    a.wait_ns = wait_limit_ns();
+    return from_cuda(launch_product(maps, a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_blocks_workspace_bytes(moe_dims_t dims) { return dims_ok_blocks(dims) ? blocks_ws(dims).total : 0; }
+
+moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weights_t weights, moe_dims_t dims,
+                                   moe_lists_t lists, void *y, int32_t y_type, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    const moe_block_weights_t &w = weights;
+    if (!dims_ok_blocks(dims) || !dtype_ok(x_type) || !dtype_ok(y_type)) return MOE_ERR_INVALID_ARG;
+    if (!x || !w.Wgate || !w.Sgate || !w.Wup || !w.Sup || !w.Wdown || !w.Sdown || !y) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_lists(lists);
+    if (st != MOE_OK) return st;
+    if (!al16(x) || !al16(w.Wgate) || !al16(w.Sgate) || !al16(w.Wup) || !al16(w.Sup) || !al16(w.Wdown) ||
+        !al16(w.Sdown) || !al16(y))
+        return MOE_ERR_MISALIGNED;
+    if (!ws) return MOE_ERR_WORKSPACE;
+    if (!al256(ws)) return MOE_ERR_MISALIGNED;
+    const BlocksWs L = blocks_ws(dims);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    st = check_device();
+    if (st != MOE_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *xq = seg<uint8_t>(ws, L.xq), *hq = seg<uint8_t>(ws, L.hq);
+    float *xs = seg<float>(ws, L.xs), *hs = seg<float>(ws, L.hs), *yp = seg<float>(ws, L.yp);
+    int32_t *cnt = seg<int32_t>(ws, L.cnt), *inv = seg<int32_t>(ws, L.inv);
+    const uint64_t pairs = static_cast<uint64_t>(dims.B) * dims.k;
+    ProductMaps up, down;
+    if (!encode_product_maps(&up, xq, dims.B, w.Wgate, w.Wup, dims.E, dims.d_ff, dims.d) ||
+        !encode_product_maps(&down, hq, pairs, w.Wdown, w.Wdown, dims.E, dims.d, dims.d_ff))
+        return MOE_ERR_CUDA;
+    ProductArgs a = {};
+    a.kind = PRODUCT_SWIGLU;
+    a.B = dims.B;
+    a.E = dims.E;
+    a.k = dims.k;
+    a.K = dims.d;
+    a.rows = dims.d_ff;
+    a.as = xs;
+    a.bs0 = w.Sgate;
+    a.bs1 = w.Sup;
+    a.n_active = lists.n_active;
+    a.active = lists.active;
+    a.offsets = lists.offsets;
+    a.tok = lists.tok;
+    a.hq = hq;
+    a.hs = hs;
+    a.cnt = cnt;
+    a.inv = inv;
+    a.error = &static_cast<BlocksControl *>(ws)->error;
+    a.wait_ns = wait_limit_ns();
+    st = from_cuda(launch_quantize(x, x_type, 1, dims.B, dims.d, 1, xq, xs, cnt, dims.B, s));
+    if (st != MOE_OK) return st;
+    st = from_cuda(launch_product(up, a, s));
+    if (st != MOE_OK) return st;
+    a.kind = PRODUCT_OUT;
+    a.K = dims.d_ff;
+    a.rows = dims.d;
+    a.by_pair = 1;
+    a.as = hs;
+    a.bs0 = a.bs1 = w.Sdown;
+    a.out = yp;
+    st = from_cuda(launch_product(down, a, s));
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_combine(yp, lists.w, cnt, inv, dims.B, dims.d, dims.k, y, y_type == MOE_BF16, s));
 }
 
 void moe_set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns == 0 ? DEFAULT_WAIT_NS : ns, std::memory_order_relaxed); }

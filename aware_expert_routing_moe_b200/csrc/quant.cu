@@ -1,0 +1,188 @@
+// Block-scaled e4m3 quantisation and the expert FFN's combine (sm_100a).
+//
+// quantize_rows_kernel  : one scale per 128 columns of a row (activations)
+// quantize_tiles_kernel : one scale per 128 x 128 block (weights)
+// combine_kernel        : y[t] = sum of w[p] * yp[p] over the token's list
+//                         entries, in list order (no atomics: the result
+//                         does not depend on scheduling)
+//
+// A block's scale is the smallest power of two s with max|x| <= 448 s (448:
+// the largest e4m3 value), 1 for a block of zeros.  Dividing by a power of
+// two is exact, so the only rounding is the one to e4m3 (nearest even) and
+// the result is fixed bit by bit, whatever computes it.
+#include <cuda_bf16.h>
+
+#include "blocks.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned ALL = 0xffffffffu;
+
+// Exponent e of the scale 2^e for a block whose largest magnitude is top
+// (its fp32 bits): top = m 2^(x-127), 1 <= m < 2; 448 = 1.75 * 2^8, so
+// e = x - 127 - 8, plus one when m > 1.75.  Below 2^-112 the scale stays
+// 2^-120: its reciprocal must be a normal number.
+__device__ __forceinline__ int scale_exp(unsigned top_bits) {
+    if (top_bits == 0u) return 0;
+    const int e = static_cast<int>(top_bits >> 23) - 135 + ((top_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < -120 ? -120 : e;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// four values scaled by inv (a power of two) -> four e4m3 bytes
+__device__ __forceinline__ unsigned pack4(float a, float b, float c, float d, float inv) {
+    unsigned short lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+    return static_cast<unsigned>(lo) | (static_cast<unsigned>(hi) << 16);
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p) {
+    return __ldg(reinterpret_cast<const float4 *>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ unsigned abs_bits(const float4 &v) {
+    const unsigned a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
+    const unsigned c = __float_as_uint(v.z) & 0x7fffffffu, d = __float_as_uint(v.w) & 0x7fffffffu;
+    return max(max(a, b), max(c, d));
+}
+
+// A warp per block of 128 columns: four columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, long long rows, int cols, int cb,
+                                                            uint8_t *__restrict__ q, float *__restrict__ scale,
+                                                            int32_t *__restrict__ cnt, int n_cnt) {
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * 8;
+    const long long first = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (cnt != nullptr)
+        for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n_cnt; i += warps * 32) cnt[i] = 0;
+    for (long long b = first; b < rows * cb; b += warps) {
+        const long long r = b / cb;
+        const int c = static_cast<int>(b - r * cb) * BLK + lane * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < cols) v = load4<T>(x + r * cols + c);
+        const int e = scale_exp(__reduce_max_sync(ALL, abs_bits(v)));
+        if (c < cols) *reinterpret_cast<unsigned *>(q + r * cols + c) = pack4(v.x, v.y, v.z, v.w, pow2(-e));
+        if (lane == 0) scale[b] = pow2(e);
+    }
+}
+
+// A block of 256 threads per 128 x 128 tile: warp w takes rows w, w + 8, ...
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ x, int rows, int cols, int rb,
+                                                             int cb, uint8_t *__restrict__ q,
+                                                             float *__restrict__ scale) {
+    __shared__ unsigned s_top[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long tile = blockIdx.x;
+    const int bc = static_cast<int>(tile % cb), br = static_cast<int>(tile / cb % rb);
+    const long long base = tile / (static_cast<long long>(cb) * rb) * rows * cols;
+    const int c = bc * BLK + lane * 4;
+    float4 v[16];
+    unsigned top = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = br * BLK + warp + 8 * i;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && c < cols) v[i] = load4<T>(x + base + static_cast<long long>(r) * cols + c);
+        top = max(top, abs_bits(v[i]));
+    }
+    top = __reduce_max_sync(ALL, top);
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, s_top[i]);
+    const int e = scale_exp(top);
+    const float inv = pow2(-e);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = br * BLK + warp + 8 * i;
+        if (r < rows && c < cols)
+            *reinterpret_cast<unsigned *>(q + base + static_cast<long long>(r) * cols + c) =
+                pack4(v[i].x, v[i].y, v[i].z, v[i].w, inv);
+    }
+    if (threadIdx.x == 0) scale[tile] = pow2(e);
+}
+
+// One block per token.
+__global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ yp, const float *__restrict__ w,
+                                                      const int32_t *__restrict__ cnt,
+                                                      const int32_t *__restrict__ inv, int d, int k,
+                                                      void *__restrict__ y, int y_bf16) {
+    __shared__ int s_p[K_MAX];
+    __shared__ float s_w[K_MAX];
+    const int t = blockIdx.x;
+    const int n = min(cnt[t], k);
+    if (threadIdx.x < n) {  // entries in ascending order
+        const int p = inv[static_cast<size_t>(t) * k + threadIdx.x];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += inv[static_cast<size_t>(t) * k + j] < p ? 1 : 0;
+        s_p[rank] = p;
+        s_w[rank] = w[p];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < d; c += blockDim.x * 4) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < n; ++j) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(yp + static_cast<size_t>(s_p[j]) * d + c));
+            s.x = fmaf(s_w[j], v.x, s.x);
+            s.y = fmaf(s_w[j], v.y, s.y);
+            s.z = fmaf(s_w[j], v.z, s.z);
+            s.w = fmaf(s_w[j], v.w, s.w);
+        }
+        const size_t at = static_cast<size_t>(t) * d + c;
+        if (y_bf16) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+            uint2 o;
+            o.x = *reinterpret_cast<const unsigned *>(&lo);
+            o.y = *reinterpret_cast<const unsigned *>(&hi);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(y) + at) = o;
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(y) + at) = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows, int64_t cols, int block_rows,
+                            uint8_t *q, float *scale, int32_t *cnt, int n_cnt, cudaStream_t s) {
+    const int cb = blocks_of(static_cast<int>(cols)), c = static_cast<int>(cols);
+    if (block_rows == 1) {
+        const long long blocks = batch * rows * cb;
+        const unsigned grid = static_cast<unsigned>(blocks + 7 < 8 * 148 * 16 ? (blocks + 7) / 8 : 148 * 16);
+        if (type == MOE_BF16)
+            quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), batch * rows, c, cb, q,
+                                                      scale, cnt, n_cnt);
+        else
+            quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), batch * rows, c, cb, q, scale,
+                                                      cnt, n_cnt);
+        return cudaGetLastError();
+    }
+    const int rb = blocks_of(static_cast<int>(rows)), r = static_cast<int>(rows);
+    const unsigned grid = static_cast<unsigned>(batch * rb * cb);
+    if (type == MOE_BF16)
+        quantize_tiles_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), r, c, rb, cb, q, scale);
+    else
+        quantize_tiles_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), r, c, rb, cb, q, scale);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const float *yp, const float *w, const int32_t *cnt, const int32_t *inv, int B, int d,
+                           int k, void *y, int y_bf16, cudaStream_t s) {
+    const int threads = d >= 1024 ? 256 : 64;
+    combine_kernel<<<B, threads, 0, s>>>(yp, w, cnt, inv, d, k, y, y_bf16);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

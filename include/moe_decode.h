@@ -314,6 +314,111 @@ moe_status_t moe_expert_ffn_channels(const float *x, const uint16_t *Wgate, cons
                                      const float *sel_w, const float *score, int32_t c, float *y,
                                      uint32_t *keep, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Routing with scores, balance bias and expert groups -----------------
+ * The general router of expert layers, for any number of tokens (a decode
+ * batch or a prefill chunk).  dims: 1 <= B <= 65536, 1 <= k <= 16,
+ * k <= E <= 512; d and d_ff are ignored. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* s = softmax(logits) over all E experts */
+    MOE_SCORE_SIGMOID = 1  /* s = 1 / (1 + exp(-logits)) */
+} moe_score_t;
+
+/* groups: the experts form `groups` runs of E / groups (1 = no groups;
+ * groups <= 32, E % groups == 0); top_groups: groups a token may use
+ * (1 <= top_groups <= groups); group_best: 1 or 2, the experts whose values
+ * a group's value sums; renorm: 0 or 1; scale: finite, > 0. */
+typedef struct {
+    int32_t score, groups, top_groups, group_best, renorm;
+    float scale;
+} moe_scoring_t;
+
+/* Device workspace bytes of moe_route_scored (0 if dims are invalid). */
+size_t moe_route_workspace_bytes(moe_dims_t dims);
+
+/* Choice of experts and per-expert token lists from router logits.
+ *   logits[B][E] fp32; bias[E] fp32 (device; NULL = none);
+ *   c_e = s_e + bias_e ranks experts (the bias steers the choice only).
+ *   groups > 1: a group's value is the sum of the group_best largest c_e in
+ *   it (of those it has); the top_groups groups of largest value (equal
+ *   values to the lower group) stay.  sel_idx[B][k] int32 = the k largest
+ *   c_e among the remaining experts, descending, equal values to the lower
+ *   index; sel_w[B][k] fp32 = s of the chosen (divided by their sum with
+ *   renorm) times scale; lists as moe_reselect writes them.
+ * A logit of -inf (or NaN) takes its expert out of the token's choice, +inf
+ * counts as the largest finite value; a token with fewer than k experts to
+ * choose from gets -1 and weight 0 in the slots left (a token with none is
+ * in no list: padding).  bias must be finite.  The choice follows the exact
+ * values of c as far as fp64 tells them apart (a comparison that fp32
+ * cannot decide is decided in fp64), so it does not depend on rounding.
+ * Deterministic.  ws: moe_route_workspace_bytes(dims) bytes (no zeroing
+ * needed). */
+moe_status_t moe_route_scored(const float *logits, const float *bias, moe_dims_t dims, moe_scoring_t rule,
+                              int32_t *sel_idx, float *sel_w, moe_lists_t lists, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/* ---- Block-scaled 8-bit experts ------------------------------------------
+ * e4m3 matrices with an fp32 scale per block of 128 columns: of one row for
+ * activations ([rows][ceil(cols / 128)]), of 128 rows for weights
+ * ([ceil(rows / 128)][ceil(cols / 128)] per matrix).  Element = value *
+ * scale.  Last blocks may be short.  dims of these entry points:
+ * 1 <= B <= 65536, 1 <= k <= 16, k <= E <= 512, d % 16 == 0 and
+ * d_ff % 16 == 0, both 16 .. 16384. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype_t;
+
+/* q[batch][rows][cols] e4m3 and scales of x[batch][rows][cols] (moe_dtype_t
+ * type; device).  block_rows: 1 (scale[batch][rows][ceil(cols / 128)]) or
+ * 128 (scale[batch][ceil(rows / 128)][ceil(cols / 128)]).  A block's scale
+ * is the smallest power of two s with max|x| <= 448 s (1 for zeros, at
+ * least 2^-120), q = x / s rounded to nearest even: the only rounding, so
+ * the result is exact bit by bit.  batch, rows >= 1, batch * rows < 2^31,
+ * cols % 16 == 0, 16 <= cols <= 16384 * 4, at most 2^31 - 1 blocks.
+ * Needs no workspace. */
+moe_status_t moe_quantize_blocks(const void *x, int32_t type, int64_t batch, int64_t rows, int64_t cols,
+                                 int32_t block_rows, uint8_t *q, float *scale, void *stream);
+
+#define MOE_GEMM_WORKSPACE_BYTES 4096
+
+/* Grouped product: y[p] = W[e] x[tok[p]] for every list entry p of expert e
+ * (lists as moe_reselect and moe_route_scored write them; w is not read).
+ * One expert that lists every token makes it a plain product.
+ *   q[B][d] e4m3 with scale[B][ceil(d / 128)]; W[E][d_ff][d] e4m3 with
+ *   Wscale[E][ceil(d_ff / 128)][ceil(d / 128)] (any finite scales);
+ *   y[B * k][d_ff] of y_type (moe_dtype_t); rows past the last list entry
+ *   are left as they were.
+ * Sums are fp32, rounded once at the end.  The result does not depend on
+ * scheduling.  ws: MOE_GEMM_WORKSPACE_BYTES bytes, 256-byte aligned,
+ * zero-filled once (its error word is moe_check_error's). */
+moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const uint8_t *W, const float *Wscale,
+                                    moe_dims_t dims, moe_lists_t lists, void *y, int32_t y_type, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/* One layer's expert weights: e4m3 Wgate, Wup [E][d_ff][d], Wdown [E][d][d_ff]
+ * and their block scales (device pointers). */
+typedef struct {
+    const uint8_t *Wgate;
+    const float *Sgate;
+    const uint8_t *Wup;
+    const float *Sup;
+    const uint8_t *Wdown;
+    const float *Sdown;
+} moe_block_weights_t;
+
+/* Device workspace bytes of moe_expert_ffn_blocks (0 if dims are invalid). */
+size_t moe_blocks_workspace_bytes(moe_dims_t dims);
+
+/* moe_expert_ffn on block-scaled 8-bit weights:
+ *   y[t] = sum over (t, e, w) entries of w * Wdown[e] h,
+ *   h = silu(Wgate[e] x_t) * (Wup[e] x_t);
+ * x[B][d] and h are rounded to e4m3 in blocks of 128 columns as
+ * moe_quantize_blocks does (the format's 8-bit operands), sums are fp32,
+ * y[B][d] is rounded once.  x_type, y_type: moe_dtype_t.  y is overwritten
+ * (0 for a token in no list).  A token's entries are added in list order:
+ * the result does not depend on scheduling.  ws: moe_blocks_workspace_bytes
+ * bytes, 256-byte aligned, zero-filled once before its first use. */
+moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weights_t weights, moe_dims_t dims,
+                                   moe_lists_t lists, void *y, int32_t y_type, void *ws, size_t ws_bytes,
+                                   void *stream);
+
 /* moe_expert_ffn for callers that cannot allocate device memory.
  * (The source pages have no counterpart to this entry point; it is a
  * deployment convenience of this library.)
