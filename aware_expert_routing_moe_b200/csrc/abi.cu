@@ -183,6 +183,24 @@ moe_lists_t ws_lists(void *ws, const WsLayout &L) {
     return l;
 }
 
+// What the phases of a block-scaled product share.
+ProductArgs product_args(const moe_dims_t &d, const moe_lists_t &l, void *ws) {
+    ProductArgs a = {};
+    BlocksControl *c = static_cast<BlocksControl *>(ws);
+    a.B = d.B;
+    a.E = d.E;
+    a.k = d.k;
+    a.n_active = l.n_active;
+    a.active = l.active;
+    a.offsets = l.offsets;
+    a.tok = l.tok;
+    a.error = &c->error;
+    a.next_tile = &c->next_tile;
+    a.exits = &c->exits;
+    a.wait_ns = wait_limit_ns();
+    return a;
+}
+
 // The most experts a call under `rule` can activate: the union of every
 // token's candidates (OEA: its first k0; top-k and the affinity rule: its
 // k), at most the budget for the XShare rules, at most E.
@@ -253,27 +271,29 @@ bool encode_expert_maps(ExpertMaps *m, const moe_dims_t &d, const uint16_t *Wgat
                                       gu_chunks));
 }
 
-bool encode_product_maps(ProductMaps *m, const void *a, uint64_t a_rows, const void *b0, const void *b1,
-                         uint64_t E, uint64_t rows, uint64_t K) {
+bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
+                       uint64_t E, uint64_t rows, uint64_t K) {
     std::memset(m, 0, sizeof(*m));
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint32_t one[3] = {1, 1, 1};
-    // activation rows: boxes of one row, gathered four at a time
     cuuint64_t adim[2] = {K, a_rows}, astride[1] = {K};
-    cuuint32_t abox[2] = {BLK, 1};
-    if (fn(&m->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(a), adim, astride, abox, one,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    CUtensorMap *amap[2] = {&m->a, &m->ab};
+    for (int i = 0; i < 2; ++i) {
+        cuuint32_t abox[2] = {BLK, i == 0 ? 1u : static_cast<cuuint32_t>(box_rows)};
+        if (fn(amap[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(a), adim, astride, abox, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
     // weights: boxes of 128 rows x 128 bytes; rows and columns past the end
     // of a matrix read as zero
     cuuint64_t bdim[3] = {K, rows, E}, bstride[2] = {K, rows * K};
     cuuint32_t bbox[3] = {BLK, BLK, 1};
     const void *b[2] = {b0, b1};
-    CUtensorMap *out[2] = {&m->b0, &m->b1};
+    CUtensorMap *bmap[2] = {&m->b0, &m->b1};
     for (int i = 0; i < 2; ++i)
-        if (fn(out[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(b[i]), bdim, bstride, bbox, one,
+        if (fn(bmap[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(b[i]), bdim, bstride, bbox, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
@@ -289,14 +309,17 @@ bool encode_router_maps(RouterMaps *m, const moe_dims_t &d, const float *x, cons
 
 BlocksWs blocks_ws(const moe_dims_t &d) {
     BlocksWs w;
-    const size_t B = d.B, k = d.k, D = d.d, F = d.d_ff, P = B * k;
+    const size_t B = d.B, E = d.E, k = d.k, D = d.d, F = d.d_ff, P = B * k;
     size_t o = MOE_GEMM_WORKSPACE_BYTES;
-    w.xq = o;  o += round_up(B * D);
-    w.xs = o;  o += round_up(B * blocks_of(d.d) * 4);
+    const size_t rows = d.B > DISPATCH_MIN ? P : B;  // quantised activation rows
+    w.xq = o;  o += round_up(rows * D);
+    w.xs = o;  o += round_up(rows * blocks_of(d.d) * 4);
     w.hq = o;  o += round_up(P * F);
     w.hs = o;  o += round_up(P * blocks_of(d.d_ff) * 4);
     w.yp = o;  o += round_up(P * D * 4);
-    w.cnt = o; o += round_up(B * 4);
+    // m-tiles: one per 128 entries, and a short one per active expert at most
+    w.n_counts = B + (P / 128 + (E < P ? E : P));
+    w.counts = o; o += round_up(w.n_counts * 4);
     w.inv = o; o += round_up(P * 4);
     w.total = o;
     return w;
@@ -560,7 +583,7 @@ moe_status_t moe_quantize_blocks(const void *x, int32_t type, int64_t batch, int
     if (!al16(x) || !al16(q) || !al16(scale)) return MOE_ERR_MISALIGNED;
     const moe_status_t st = check_device();
     if (st != MOE_OK) return st;
-    return from_cuda(launch_quantize(x, type, batch, rows, cols, block_rows, q, scale, nullptr, 0,
+    return from_cuda(launch_quantize(x, type, batch, rows, cols, block_rows, q, scale,
                                      static_cast<cudaStream_t>(stream)));
 }
 
@@ -578,24 +601,21 @@ moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const 
     st = check_device();
     if (st != MOE_OK) return st;
     ProductMaps maps;
-    if (!encode_product_maps(&maps, q, dims.B, W, W, dims.E, dims.d_ff, dims.d)) return MOE_ERR_CUDA;
-    ProductArgs a = {};
-    a.kind = PRODUCT_OUT;
-    a.B = dims.B;
-    a.E = dims.E;
-    a.k = dims.k;
-    a.K = dims.d;
-    a.rows = dims.d_ff;
-    a.as = scale;
-    a.bs0 = a.bs1 = Wscale;
-    a.n_active = lists.n_active;
-    a.active = lists.active;
-    a.offsets = lists.offsets;
-    a.tok = lists.tok;
-    a.out = y;
-    a.out_bf16 = y_type == MOE_BF16;
-    a.error = &static_cast<BlocksControl *>(ws)->error;
-    a.wait_ns = wait_limit_ns();
+    std::memset(&maps, 0, sizeof(maps));
+    if (!encode_phase_maps(&maps.phase[0], q, dims.B, product_box_rows(dims.B), W, W, dims.E, dims.d_ff, dims.d))
+        return MOE_ERR_CUDA;
+    ProductArgs a = product_args(dims, lists, ws);
+    a.phases = 1;
+    ProductPhase &p = a.phase[0];
+    p.kind = PRODUCT_OUT;
+    p.K = dims.d;
+    p.rows = dims.d_ff;
+    p.as = scale;
+    p.as_row = blocks_of(dims.d);
+    p.as_col = 1;
+    p.bs0 = p.bs1 = Wscale;
+    p.out = y;
+    p.out_bf16 = y_type == MOE_BF16;
     return from_cuda(launch_product(maps, a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -621,46 +641,46 @@ moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weig
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *xq = seg<uint8_t>(ws, L.xq), *hq = seg<uint8_t>(ws, L.hq);
     float *xs = seg<float>(ws, L.xs), *hs = seg<float>(ws, L.hs), *yp = seg<float>(ws, L.yp);
-    int32_t *cnt = seg<int32_t>(ws, L.cnt), *inv = seg<int32_t>(ws, L.inv);
-    const uint64_t pairs = static_cast<uint64_t>(dims.B) * dims.k;
-    ProductMaps up, down;
-    if (!encode_product_maps(&up, xq, dims.B, w.Wgate, w.Wup, dims.E, dims.d_ff, dims.d) ||
-        !encode_product_maps(&down, hq, pairs, w.Wdown, w.Wdown, dims.E, dims.d, dims.d_ff))
+    int32_t *counts = seg<int32_t>(ws, L.counts), *inv = seg<int32_t>(ws, L.inv);
+    const int pairs = dims.B * dims.k;
+    const bool dispatch = dims.B > DISPATCH_MIN;
+    const int rows = dispatch ? pairs : dims.B, box = product_box_rows(dims.B);
+    ProductMaps maps;
+    if (!encode_phase_maps(&maps.phase[0], xq, rows, box, w.Wgate, w.Wup, dims.E, dims.d_ff, dims.d) ||
+        !encode_phase_maps(&maps.phase[1], hq, pairs, box, w.Wdown, w.Wdown, dims.E, dims.d, dims.d_ff))
         return MOE_ERR_CUDA;
-    ProductArgs a = {};
-    a.kind = PRODUCT_SWIGLU;
-    a.B = dims.B;
-    a.E = dims.E;
-    a.k = dims.k;
-    a.K = dims.d;
-    a.rows = dims.d_ff;
-    a.as = xs;
-    a.bs0 = w.Sgate;
-    a.bs1 = w.Sup;
-    a.n_active = lists.n_active;
-    a.active = lists.active;
-    a.offsets = lists.offsets;
-    a.tok = lists.tok;
-    a.hq = hq;
-    a.hs = hs;
-    a.cnt = cnt;
+    ProductArgs a = product_args(dims, lists, ws);
+    a.phases = 2;
+    a.cnt = counts;
+    a.done = counts + dims.B;
     a.inv = inv;
-    a.error = &static_cast<BlocksControl *>(ws)->error;
-    a.wait_ns = wait_limit_ns();
-    st = from_cuda(launch_quantize(x, x_type, 1, dims.B, dims.d, 1, xq, xs, cnt, dims.B, s));
+    ProductPhase &up = a.phase[0], &down = a.phase[1];
+    up.kind = PRODUCT_SWIGLU;
+    up.K = dims.d;
+    up.rows = dims.d_ff;
+    up.by_pair = dispatch;
+    up.as = xs;
+    up.as_row = 1;
+    up.as_col = rows;
+    up.bs0 = w.Sgate;
+    up.bs1 = w.Sup;
+    up.hq = hq;
+    up.hs = hs;
+    down.kind = PRODUCT_OUT;
+    down.K = dims.d_ff;
+    down.rows = dims.d;
+    down.by_pair = 1;
+    down.as = hs;
+    down.as_row = 1;
+    down.as_col = pairs;
+    down.bs0 = down.bs1 = w.Sdown;
+    down.out = yp;
+    st = from_cuda(launch_quantize_dispatch(x, x_type, rows, dims.d, dispatch ? lists.tok : nullptr, dims.B, xq, xs,
+                                            counts, static_cast<int>(L.n_counts), s));
     if (st != MOE_OK) return st;
-    st = from_cuda(launch_product(up, a, s));
+    st = from_cuda(launch_product(maps, a, s));
     if (st != MOE_OK) return st;
-    a.kind = PRODUCT_OUT;
-    a.K = dims.d_ff;
-    a.rows = dims.d;
-    a.by_pair = 1;
-    a.as = hs;
-    a.bs0 = a.bs1 = w.Sdown;
-    a.out = yp;
-    st = from_cuda(launch_product(down, a, s));
-    if (st != MOE_OK) return st;
-    return from_cuda(launch_combine(yp, lists.w, cnt, inv, dims.B, dims.d, dims.k, y, y_type == MOE_BF16, s));
+    return from_cuda(launch_combine(yp, lists.w, a.cnt, inv, dims.B, dims.d, dims.k, y, y_type == MOE_BF16, s));
 }
 
 void moe_set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns == 0 ? DEFAULT_WAIT_NS : ns, std::memory_order_relaxed); }

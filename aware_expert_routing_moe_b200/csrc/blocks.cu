@@ -14,11 +14,20 @@
 // share a block).  Two TMEM buffers of 256 columns let the MMAs of the next
 // column block run while one is added.
 //
-// Persistent CTAs, one per SM, take tiles round robin.  Roles: warps 0-7
-// epilogue, warp 8 loads (weights as TMA boxes, activation rows gathered
-// four at a time by list entry), warp 9 issues the MMAs.  Every wait is
-// bounded; past the limit the CTA records an error, lets its copies and
-// MMAs land and leaves.
+// A call is one phase (a plain product) or two (gate/up, then down, whose
+// activations are the first phase's h).  Persistent CTAs, one per SM, claim
+// tiles from a counter, all of the first phase's before the second's; a down
+// tile waits until its entries' gate/up tiles are counted done.  A tile is
+// claimed only by a running CTA, so no wait depends on a CTA that has not
+// started.  The last CTA puts the counters back to zero.
+//
+// Roles: warps 0-7 epilogue; warp 8 weights (TMA boxes; they do not wait for
+// the tile's activations); warp 9 MMAs; warp 10 activation rows (a box, or
+// gathered four at a time by list entry) and the scales of each column
+// block, copied to a ring of their own, so that no global load latency sits
+// in the epilogue's loop; warp 11 claims tiles.  Every wait is bounded; past
+// the limit the CTA records an error, lets its copies and MMAs land and
+// leaves.
 #include <cuda_bf16.h>
 
 #include "blocks.h"
@@ -31,35 +40,65 @@ constexpr unsigned ALL = 0xffffffffu;
 constexpr int TILE_M = 128;       // list entries per tile
 constexpr int TILE_N = 256;       // weight rows per tile (128 + 128 for gate/up)
 constexpr int W_STAGE = TILE_N * BLK;  // weight bytes of a stage: 256 rows x 128 columns
-constexpr int A_STAGE = TILE_M * BLK;
-constexpr int STAGE = W_STAGE + A_STAGE;
-constexpr int STAGES = 4;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = (EPI_WARPS + 2) * 32;
+constexpr int THREADS = (EPI_WARPS + 4) * 32;
+// Registers a thread: the block starts with 168 (384 threads); the four
+// copy and issue warps give theirs up for the epilogue's accumulators.
+constexpr int REGS_EPI = 224, REGS_COPY = 56;
+static_assert(256 * REGS_EPI + 128 * REGS_COPY <= THREADS * 168, "register split");
 constexpr int OUT_PITCH = 80;     // bytes of a staged output row: 64 and a pad that spreads the banks
 constexpr int OUT_STAGE = 32 * OUT_PITCH;
-constexpr unsigned long long DRAIN_NS = 1000000000ull;
+constexpr int SCALES = 8;         // column blocks whose scales are in flight
+constexpr int TILES = 2;          // tiles claimed ahead
+constexpr int GATHER_MAX = 32;    // rows that are gathered although they are consecutive
+constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
+
+// Batches of up to AR tokens (no expert has more entries) keep AR rows of
+// activations per stage, which leaves room for a fifth stage.
+template <int AR>
+struct Ring {
+    static constexpr int A_STAGE = AR * BLK;
+    static constexpr int STAGE = W_STAGE + A_STAGE;
+    static constexpr int STAGES = AR == TILE_M ? 4 : 5;
+    static constexpr int OUT_STAGES = AR / 32 * 2;  // epilogue warps that can hold rows
+};
+
+enum : int { TILE_END = 2 };
+struct Tile {
+    int phase, e, p0, n, nb, mt;  // phase (TILE_END: no more), expert, first entry, entries, column tile, m-tile
+};
 
 struct Ctl {
-    unsigned long long full[STAGES], empty[STAGES];
+    unsigned long long full[5], empty[5];
     unsigned long long part_full[2], part_free[2];
+    unsigned long long scale_full[SCALES], scale_free[SCALES];
+    unsigned long long tile_full[TILES], tile_free[TILES];
     unsigned long long mma_done;
     volatile int abort_flag;
-    int n_slots, n_tiles;
+    int n_slots, m_tiles;
+    unsigned fills[2];  // stages filled with weights, with rows
     uint32_t tmem;
-    float top[2][2][TILE_M];  // [tile parity][column half][row]: largest |h|
+    Tile tile[TILES];
+    float scale[SCALES][TILE_M + 4];  // 128 row scales, then the two weight blocks'
+    float top[2][2][TILE_M];          // [tile parity][column half][row]: largest |h|
     int act[SE_MAX], off[SE_MAX + 1], mt[SE_MAX + 1];  // expert, first entry, first m-tile of a slot
 };
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE + EPI_WARPS * OUT_STAGE + static_cast<int>(sizeof(Ctl));
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+template <int AR>
+constexpr int smem_bytes() {
+    return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_STAGES * OUT_STAGE + static_cast<int>(sizeof(Ctl));
+}
+static_assert(smem_bytes<128>() <= 232448 - 64 && smem_bytes<64>() <= 232448 - 64, "shared memory budget");
+// an MMA reads 128 activation rows: those past a 64-row region are bytes of
+// the next region (their sums are not used)
+static_assert((TILE_M - 64) * BLK <= Ring<64>::OUT_STAGES * OUT_STAGE, "the last stage's operand must end inside the block's memory");
 
 // ---------------------------------------------------------------- PTX --
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ unsigned long long clock_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
+// Time for the bounded waits: SM cycles at the highest clock, so that a limit
+// is never shorter than asked for (reading the global timer instead costs
+// every wait that does not succeed at once several hundred nanoseconds).
+constexpr unsigned long long CYCLES_PER_NS = 2;
+__device__ __forceinline__ unsigned long long cycles() { return static_cast<unsigned long long>(clock64()); }
 __device__ __forceinline__ void bar_init(unsigned long long *b, unsigned n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory");
 }
@@ -68,6 +107,32 @@ __device__ __forceinline__ void bar_expect(unsigned long long *b, unsigned bytes
 }
 __device__ __forceinline__ void bar_arrive(unsigned long long *b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+// four bytes global -> shared; arrive on b when this thread's copies land
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(saddr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(unsigned long long *b) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int32_t *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void add_release(int32_t *p) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+// orders generic-proxy accesses with the TMA copies of this or another CTA
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// c (two floats) += a (two floats) * b
+__device__ __forceinline__ void fma2(float &c0, float &c1, uint32_t a0, uint32_t a1, float b) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "r"(a0), "r"(a1), "f"(b));
 }
 __device__ __forceinline__ bool bar_try(unsigned long long *b, unsigned parity) {
     unsigned ok;
@@ -86,6 +151,13 @@ __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int 
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst)),
         "l"(reinterpret_cast<unsigned long long>(map)), "r"(c), "r"(r), "r"(e), "r"(saddr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void load_rows(void *dst, const CUtensorMap *map, int c, int r, unsigned long long *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(saddr(dst)),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(c), "r"(r), "r"(saddr(bar))
         : "memory");
 }
 __device__ __forceinline__ void load_rows4(void *dst, const CUtensorMap *map, int c, const int (&r)[4],
@@ -134,27 +206,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 
 // Bounded wait on an mbarrier phase; false once the CTA has given up.
-__device__ bool wait_bar(unsigned long long *b, unsigned parity, Ctl *ctl, const ProductArgs &a, int code) {
-    if (bar_try(b, parity)) return true;
-    const unsigned long long t0 = clock_ns();
+__device__ __forceinline__ bool wait_slow(unsigned long long *b, unsigned parity, Ctl *ctl, const ProductArgs &a, int code) {
+    const unsigned long long t0 = cycles();
     for (;;) {
         if (bar_try(b, parity)) return true;
         if (ctl->abort_flag) return false;
-        if (clock_ns() - t0 > a.wait_ns) {
+        if (cycles() - t0 > a.wait_ns * CYCLES_PER_NS) {
             atomicCAS(a.error, 0, code);
             ctl->abort_flag = 1;
             return false;
         }
     }
 }
+__device__ __forceinline__ bool wait_bar(unsigned long long *b, unsigned parity, Ctl *ctl, const ProductArgs &a,
+                                         int code) {
+    return bar_try(b, parity) || wait_slow(b, parity, ctl, a, code);
+}
 
 // --------------------------------------------------------------- tiles --
-struct Tile {
-    int slot, e, p0, n, nb;  // slot, expert, first entry, entries, column tile
-};
-// Tile t: slots in order, within a slot the column tiles, within one the
-// m-tiles (neighbouring CTAs then share weights in L2).
-__device__ __forceinline__ Tile tile_at(int t, int nbt, const Ctl *ctl) {
+// Tile t of a phase with nbt column tiles: slots in order, within a slot the
+// column tiles, within one the m-tiles (CTAs that run together then share
+// weights in L2).  A slot without entries holds no m-tile: the search takes
+// the last slot whose first m-tile is at most t / nbt.
+__device__ Tile tile_at(int t, int phase, int nbt, const Ctl *ctl) {
     int lo = 0, hi = ctl->n_slots - 1;
     const int v = t / nbt;
     while (lo < hi) {
@@ -165,21 +239,19 @@ __device__ __forceinline__ Tile tile_at(int t, int nbt, const Ctl *ctl) {
     const int mts = ctl->mt[lo + 1] - ctl->mt[lo];
     const int r = t - ctl->mt[lo] * nbt;
     Tile x;
-    x.slot = lo;
+    x.phase = phase;
     x.e = ctl->act[lo];
     x.nb = r / mts;
     const int m = r - x.nb * mts;
+    x.mt = ctl->mt[lo] + m;
     x.p0 = ctl->off[lo] + m * TILE_M;
     x.n = min(TILE_M, ctl->off[lo + 1] - x.p0);
     return x;
 }
 
-// Slots with no entries hold no m-tile; the search above never lands on one
-// because it takes the last slot whose first m-tile is at most v.
-
 // The call's slots from the lists, checked before anything indexes with
 // them: inconsistent lists run as an empty call and are recorded.
-__device__ void build_slots(Ctl *ctl, const ProductArgs &a, int nbt) {
+__device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
     __shared__ int s_bad;
     const int most = min(a.E, a.B * a.k);
     if (threadIdx.x == 0) s_bad = 0;
@@ -219,96 +291,223 @@ __device__ void build_slots(Ctl *ctl, const ProductArgs &a, int nbt) {
         if (threadIdx.x == 0) {
             ctl->mt[n] = run;
             ctl->n_slots = n;
-            ctl->n_tiles = run * nbt;
+            ctl->m_tiles = run;
             if (s_bad && blockIdx.x == 0) atomicCAS(a.error, 0, DEV_BAD_LISTS);
         }
     }
     __syncthreads();
 }
 
-// --------------------------------------------------------------- roles --
-__device__ void producer(unsigned char *ring, Ctl *ctl, const ProductMaps &maps, const ProductArgs &a, int nbt,
-                         int kb) {
-    const int lane = threadIdx.x & 31;
-    const int last_row = (a.by_pair ? a.B * a.k : a.B) - 1;
-    unsigned it = 0;
-    for (int t = blockIdx.x; t < ctl->n_tiles; t += gridDim.x) {
-        const Tile x = tile_at(t, nbt, ctl);
-        int rows[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // rows past the tile's end repeat its last one (their sums are not used)
-            const int p = x.p0 + min(lane * 4 + j, x.n - 1);
-            int r = a.by_pair ? p : __ldg(a.tok + p);
-            if (r < 0 || r > last_row) {
-                atomicCAS(a.error, 0, DEV_BAD_LISTS);
-                r = 0;
-            }
-            rows[j] = r;
-        }
-        const int groups = (x.n + 3) >> 2;
-        const int r0 = a.kind == PRODUCT_SWIGLU ? x.nb * BLK : x.nb * TILE_N;
-        const int r1 = a.kind == PRODUCT_SWIGLU ? r0 : r0 + BLK;
-        for (int j = 0; j < kb; ++j, ++it) {
-            const int st = it % STAGES;
-            unsigned char *w = ring + st * STAGE;
-            const bool ok = it < STAGES || wait_bar(&ctl->empty[st], ((it / STAGES) - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY);
-            if (!__all_sync(ALL, ok)) goto drain;
-            if (lane == 0) {
-                bar_expect(&ctl->full[st], W_STAGE + groups * 4 * BLK);
-                load_box(w, &maps.b0, j * BLK, r0, x.e, &ctl->full[st]);
-                load_box(w + W_STAGE / 2, &maps.b1, j * BLK, r1, x.e, &ctl->full[st]);
-            }
-            __syncwarp();
-            if (lane < groups) load_rows4(w + W_STAGE + lane * 4 * BLK, &maps.a, j * BLK, rows, &ctl->full[st]);
-            __syncwarp();
-        }
-    }
-drain:
-    // copies in flight land before the CTA's shared memory goes away
-    if (lane == 0) {
-        const unsigned long long t0 = clock_ns();
-        for (unsigned i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-            while (!bar_try(&ctl->full[i % STAGES], (i / STAGES) & 1) && clock_ns() - t0 < DRAIN_NS) {
-            }
-    }
-    __syncwarp();
+__device__ __forceinline__ int column_tiles(const ProductPhase &p) {
+    return p.kind == PRODUCT_SWIGLU ? (p.rows + BLK - 1) / BLK : (p.rows + TILE_N - 1) / TILE_N;
 }
 
-__device__ void issuer(unsigned char *ring, Ctl *ctl, const ProductArgs &a, int kb) {
+// The next tile of the CTA's sequence; false: none (or given up).
+struct TileCursor {
+    unsigned i = 0;
+    __device__ __forceinline__ bool next(Ctl *ctl, const ProductArgs &a, Tile &x) {
+        const int s = i % TILES;
+        if (!wait_bar(&ctl->tile_full[s], (i / TILES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return false;
+        x = ctl->tile[s];
+        return true;
+    }
+    __device__ __forceinline__ void release(Ctl *ctl) {
+        bar_arrive(&ctl->tile_free[i % TILES]);
+        ++i;
+    }
+};
+
+// --------------------------------------------------------------- roles --
+__device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
+    const int nbt0 = column_tiles(a.phase[0]), t0 = ctl->m_tiles * nbt0;
+    const int nbt1 = a.phases > 1 ? column_tiles(a.phase[1]) : 0, total = t0 + ctl->m_tiles * nbt1;
+    for (unsigned i = 0;; ++i) {
+        const int s = i % TILES;
+        if (i >= TILES && !wait_bar(&ctl->tile_free[s], (i / TILES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY)) return;
+        const int t = atomicAdd(a.next_tile, 1);
+        Tile x;
+        x.phase = TILE_END;
+        if (t < t0) x = tile_at(t, 0, nbt0, ctl);
+        else if (t < total) x = tile_at(t - t0, 1, nbt1, ctl);
+        ctl->tile[s] = x;
+        bar_arrive(&ctl->tile_full[s]);
+        if (x.phase == TILE_END) return;
+    }
+}
+
+// Lets the copies in flight land before the CTA leaves: after a wait that ran
+// out, one of the two copying roles may have filled stages that the other has
+// not; its arrival is made up for.
+template <int STAGES>
+__device__ void drain_fills(Ctl *ctl) {
+    const unsigned w = ctl->fills[0], r = ctl->fills[1], lo = min(w, r), hi = max(w, r);
+    for (unsigned i = lo; i < hi; ++i) bar_arrive(&ctl->full[i % STAGES]);
+    const unsigned long long t0 = cycles();
+    for (unsigned i = hi > STAGES ? hi - STAGES : 0; i < hi; ++i)
+        while (!bar_try(&ctl->full[i % STAGES], (i / STAGES) & 1) && cycles() - t0 < DRAIN_CYCLES) {
+        }
+}
+
+template <int AR>
+__device__ unsigned weights_role(unsigned char *ring, Ctl *ctl, const ProductMaps &maps, const ProductArgs &a) {
+    using R = Ring<AR>;
+    TileCursor cur;
+    Tile x;
     unsigned it = 0;
-    const uint32_t tmem = ctl->tmem;
-    const bool leader = elect_one();
-    for (int t = blockIdx.x; t < ctl->n_tiles; t += gridDim.x) {
+    while (cur.next(ctl, a, x)) {
+        cur.release(ctl);
+        if (x.phase == TILE_END) return it;
+        const ProductPhase &ph = a.phase[x.phase];
+        const int kb = (ph.K + BLK - 1) / BLK;
+        const int r0 = ph.kind == PRODUCT_SWIGLU ? x.nb * BLK : x.nb * TILE_N;
+        const int r1 = ph.kind == PRODUCT_SWIGLU ? r0 : r0 + BLK;
+        const CUtensorMap *m0 = &maps.phase[x.phase].b0, *m1 = &maps.phase[x.phase].b1;
         for (int j = 0; j < kb; ++j, ++it) {
-            const int st = it % STAGES, buf = it & 1;
-            bool ok = it < 2 || wait_bar(&ctl->part_free[buf], ((it >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP);
-            ok = ok && wait_bar(&ctl->full[st], (it / STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL);
-            if (!__all_sync(ALL, ok)) goto drain;
-            tc_fence_after();
-            if (leader) {
-                const uint64_t b = umma_desc(saddr(ring + st * STAGE));
-                const uint64_t x = umma_desc(saddr(ring + st * STAGE + W_STAGE));
+            const int st = it % R::STAGES;
+            unsigned char *w = ring + st * R::STAGE;
+            if (it >= R::STAGES && !wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY)) return it;
+            bar_expect(&ctl->full[st], W_STAGE);
+            load_box(w, m0, j * BLK, r0, x.e, &ctl->full[st]);
+            load_box(w + W_STAGE / 2, m1, j * BLK, r1, x.e, &ctl->full[st]);
+        }
+    }
+    return it;
+}
+
+template <int AR>
+__device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &maps, const ProductArgs &a) {
+    using R = Ring<AR>;
+    const int lane = threadIdx.x & 31;
+    TileCursor cur;
+    Tile x;
+    unsigned it = 0;
+    for (;;) {
+        if (!__all_sync(ALL, cur.next(ctl, a, x))) return it;
+        __syncwarp();
+        if (lane == 0) cur.release(ctl);
+        else ++cur.i;
+        if (x.phase == TILE_END) return it;
+        const ProductPhase &ph = a.phase[x.phase];
+        const int kb = (ph.K + BLK - 1) / BLK, rb = (ph.rows + BLK - 1) / BLK;
+        if (x.phase == 1) {
+            // the entries' gate/up tiles are all done
+            const int need = column_tiles(a.phase[0]);
+            bool ok = true;
+            if (lane == 0 && ld_acquire(a.done + x.mt) < need) {
+                const unsigned long long t0 = cycles();
+                while (ld_acquire(a.done + x.mt) < need) {
+                    ok = !ctl->abort_flag;
+                    if (ok && cycles() - t0 > a.wait_ns * CYCLES_PER_NS) {
+                        atomicCAS(a.error, 0, DEV_TIMEOUT_DEP);
+                        ctl->abort_flag = 1;
+                        ok = false;
+                    }
+                    if (!ok) break;
+                }
+            }
+            if (!__all_sync(ALL, ok)) return it;
+            fence_async();
+        }
+        // lane l copies the scales of rows l, l + 32, ..., and gathers rows 4 l ..
+        const int last = (ph.by_pair ? a.B * a.k : a.B) - 1;
+        const float *src[4];
+        int rows[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s)  // 32 columns = 32 bytes each
-                    umma_e4m3(tmem + buf * TILE_N, x + 2 * s, b + 2 * s, s > 0);
-                umma_commit(saddr(&ctl->empty[st]));
-                umma_commit(saddr(&ctl->part_full[buf]));
+        for (int q = 0; q < 4; ++q) {
+            // rows past the tile's end repeat its last one (their sums are not used)
+            const int p = x.p0 + min(lane * 4 + q, x.n - 1), ps = x.p0 + min(lane + 32 * q, x.n - 1);
+            int r = p, rs = ps;
+            if (!ph.by_pair) {
+                r = __ldg(a.tok + p);
+                rs = __ldg(a.tok + ps);
+                if (r < 0 || r > last) {
+                    atomicCAS(a.error, 0, DEV_BAD_LISTS);
+                    r = 0;
+                }
+                if (rs < 0 || rs > last) rs = 0;
+            }
+            rows[q] = r;
+            src[q] = ph.as + rs * static_cast<size_t>(ph.as_row);
+        }
+        const float *wsrc = nullptr;
+        if (lane == 0) {
+            const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : 2 * x.nb;
+            wsrc = ph.bs0 + (static_cast<size_t>(x.e) * rb + nb) * kb;
+        } else if (lane == 1) {
+            const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + 1, rb - 1);
+            wsrc = ph.bs1 + (static_cast<size_t>(x.e) * rb + nb) * kb;
+        }
+        // consecutive rows in one box; few rows, or scattered ones, four at a time
+        const int first = __shfl_sync(ALL, rows[0], 0);
+        bool run = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) run = run && rows[q] == first + min(lane * 4 + q, x.n - 1);
+        const bool box = __all_sync(ALL, run) && x.n > GATHER_MAX;
+        const int groups = (x.n + 3) >> 2;
+        const unsigned bytes = box ? R::A_STAGE : groups * 4 * BLK;
+        const CUtensorMap *m = box ? &maps.phase[x.phase].ab : &maps.phase[x.phase].a;
+        for (int j = 0; j < kb; ++j, ++it) {
+            const int st = it % R::STAGES, sc = it % SCALES;
+            unsigned char *d = ring + st * R::STAGE + W_STAGE;
+            bool ok = it < R::STAGES || wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY);
+            ok = ok && (it < SCALES || wait_bar(&ctl->scale_free[sc], (it / SCALES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY));
+            if (!__all_sync(ALL, ok)) return it;
+            if (lane == 0) {
+                bar_expect(&ctl->full[st], bytes);
+                if (box) load_rows(d, m, j * BLK, first, &ctl->full[st]);
             }
             __syncwarp();
+            if (!box && lane < groups) load_rows4(d + lane * 4 * BLK, m, j * BLK, rows, &ctl->full[st]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (lane + 32 * q < x.n) copy4(&ctl->scale[sc][lane + 32 * q], src[q] + static_cast<size_t>(j) * ph.as_col);
+            if (lane < 2) copy4(&ctl->scale[sc][TILE_M + lane], wsrc + j);
+            copies_arrive(&ctl->scale_full[sc]);
         }
     }
-drain:
-    if (leader) {
-        umma_commit(saddr(&ctl->mma_done));
-        const unsigned long long t0 = clock_ns();
-        while (!bar_try(&ctl->mma_done, 0) && clock_ns() - t0 < DRAIN_NS) {
+}
+
+template <int AR>
+__device__ void issue_role(unsigned char *ring, Ctl *ctl, const ProductArgs &a) {
+    using R = Ring<AR>;
+    const uint32_t tmem = ctl->tmem;
+    TileCursor cur;
+    Tile x;
+    unsigned it = 0;
+    while (cur.next(ctl, a, x)) {
+        cur.release(ctl);
+        if (x.phase == TILE_END) return;
+        const int kb = (a.phase[x.phase].K + BLK - 1) / BLK;
+        for (int j = 0; j < kb; ++j, ++it) {
+            const int st = it % R::STAGES, buf = it & 1;
+            if (it >= 2 && !wait_bar(&ctl->part_free[buf], ((it >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP)) return;
+            if (!wait_bar(&ctl->full[st], (it / R::STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return;
+            tc_fence_after();
+            const uint64_t b = umma_desc(saddr(ring + st * R::STAGE));
+            const uint64_t v = umma_desc(saddr(ring + st * R::STAGE + W_STAGE));
+#pragma unroll
+            for (int s = 0; s < 4; ++s)  // 32 columns = 32 bytes each
+                umma_e4m3(tmem + buf * TILE_N, v + 2 * s, b + 2 * s, s > 0);
+            umma_commit(saddr(&ctl->empty[st]));
+            umma_commit(saddr(&ctl->part_full[buf]));
         }
     }
-    __syncwarp();
 }
 
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// all epilogue threads meet; true if any of them says so
+__device__ __forceinline__ bool epi_any(bool v) {
+    unsigned r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 2, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<unsigned>(v))
+        : "memory");
+    return r != 0;
+}
 
 // 32 rows x 64 bytes of a warp's output through shared memory: lane l wrote
 // its row's four 16-byte pieces; rows go out as whole 64-byte runs.
@@ -339,68 +538,97 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
     return *reinterpret_cast<const unsigned *>(&v);
 }
 
-__device__ void epilogue(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a, int nbt, int kb) {
+// 64 output columns n0 .. of the warp's rows
+__device__ __forceinline__ void store_out(unsigned char *stage, const float (&c)[64], const ProductPhase &ph, size_t row0,
+                                          int n0, int rows_here, int lane) {
+    uint4 o[4];
+    unsigned *w = reinterpret_cast<unsigned *>(o);
+    const size_t at = row0 * ph.rows + n0;
+    if (ph.out_bf16) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(c[q * 32 + 2 * i], c[q * 32 + 2 * i + 1]);
+            store_chunk(stage, o, static_cast<char *>(ph.out) + (at + q * 32) * 2, static_cast<size_t>(ph.rows) * 2,
+                        rows_here, lane, (ph.rows - n0 - q * 32) * 2);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(c[q * 16 + i]);
+            store_chunk(stage, o, static_cast<char *>(ph.out) + (at + q * 16) * 4, static_cast<size_t>(ph.rows) * 4,
+                        rows_here, lane, (ph.rows - n0 - q * 16) * 4);
+        }
+    }
+}
+
+template <int AR>
+__device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .., columns 64 half .. of each matrix
     const int row = quarter * 32 + lane;
     const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
-    const int rb = (a.rows + BLK - 1) / BLK;
-    unsigned char *stage = out_stage + warp * OUT_STAGE;
+    unsigned char *stage = out_stage + (half * (AR / 32) + quarter) * OUT_STAGE;  // used by warps with rows
     bool dead = false;
     unsigned it = 0;
-    int parity = 0;
-    for (int t = blockIdx.x; t < ctl->n_tiles; t += gridDim.x, parity ^= 1) {
-        const Tile x = tile_at(t, nbt, ctl);
+    TileCursor cur;
+    Tile x;
+    for (;;) {
+        dead = dead || !cur.next(ctl, a, x);
+        if (epi_any(dead)) return;  // together, so that none is left at a barrier
+        __syncwarp();
+        const int parity = cur.i & 1;
+        if (lane == 0) cur.release(ctl);
+        else ++cur.i;
+        if (x.phase == TILE_END) return;
+        const ProductPhase &ph = a.phase[x.phase];
+        const int kb = (ph.K + BLK - 1) / BLK;
         const bool live = quarter * 32 < x.n;  // the warp holds rows of the tile
-        const int p = x.p0 + min(row, x.n - 1);
-        int ar = a.by_pair ? p : __ldg(a.tok + p);
-        if (ar < 0 || ar >= (a.by_pair ? a.B * a.k : a.B)) ar = 0;  // recorded by the producer
-        const float *as = a.as + static_cast<size_t>(ar) * kb;
-        const int nb0 = a.kind == PRODUCT_SWIGLU ? x.nb : 2 * x.nb;
-        const int nb1 = a.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + 1, rb - 1);
-        const float *s0 = a.bs0 + (static_cast<size_t>(x.e) * rb + nb0) * kb;
-        const float *s1 = a.bs1 + (static_cast<size_t>(x.e) * rb + nb1) * kb;
         float c0[64], c1[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) c0[i] = c1[i] = 0.0f;
-        float fa = __ldg(as), f0 = __ldg(s0), f1 = __ldg(s1);
         for (int j = 0; j < kb; ++j, ++it) {
-            const int buf = it & 1;
-            const float m0 = fa * f0, m1 = fa * f1;
-            if (j + 1 < kb) {
-                fa = __ldg(as + j + 1);
-                f0 = __ldg(s0 + j + 1);
-                f1 = __ldg(s1 + j + 1);
-            }
-            if (!__all_sync(ALL, !dead && wait_bar(&ctl->part_full[buf], (it >> 1) & 1, ctl, a, DEV_TIMEOUT_FULL)))
-                dead = true;
-            if (!dead) {
-                tc_fence_after();
-                if (live) {
-                    const uint32_t col = tbase + buf * TILE_N;
-                    uint32_t v[32];
+            const int buf = it & 1, sc = it % SCALES;
+            bool ok = !dead && wait_bar(&ctl->scale_full[sc], (it / SCALES) & 1, ctl, a, DEV_TIMEOUT_FULL);
+            ok = ok && wait_bar(&ctl->part_full[buf], (it >> 1) & 1, ctl, a, DEV_TIMEOUT_FULL);
+            dead = !__all_sync(ALL, ok);
+            if (dead) continue;
+            tc_fence_after();
+            if (live) {
+                const float fa = ctl->scale[sc][row];
+                const float m0 = fa * ctl->scale[sc][TILE_M], m1 = fa * ctl->scale[sc][TILE_M + 1];
+                const uint32_t col = tbase + buf * TILE_N;
+                uint32_t v[32];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        tmem_ld32(col + q * 32, v);
+                for (int q = 0; q < 2; ++q) {
+                    tmem_ld32(col + q * 32, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) c0[q * 32 + i] = fmaf(__uint_as_float(v[i]), m0, c0[q * 32 + i]);
-                        tmem_ld32(col + 128 + q * 32, v);
+                    for (int i = 0; i < 32; i += 2) fma2(c0[q * 32 + i], c0[q * 32 + i + 1], v[i], v[i + 1], m0);
+                    tmem_ld32(col + 128 + q * 32, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) c1[q * 32 + i] = fmaf(__uint_as_float(v[i]), m1, c1[q * 32 + i]);
-                    }
+                    for (int i = 0; i < 32; i += 2) fma2(c1[q * 32 + i], c1[q * 32 + i + 1], v[i], v[i + 1], m1);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&ctl->part_free[buf]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(&ctl->part_free[buf]);
+                bar_arrive(&ctl->scale_free[sc]);
             }
         }
         const int rows_here = min(32, x.n - quarter * 32);
-        if (a.kind == PRODUCT_SWIGLU) {
+        const size_t row0 = static_cast<size_t>(x.p0 + quarter * 32);
+        if (ph.kind == PRODUCT_SWIGLU) {
             float top = 0.0f;
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                c0[i] = c0[i] / (1.0f + expf(-c0[i])) * c1[i];
-                top = fmaxf(top, fabsf(c0[i]));
+                for (int i = 0; i < 64; ++i) {
+                    // silu(g) u; the fast exp and division are good to a few
+                    // units of fp32, and h is about to be rounded to 4 bits
+                    c0[i] = __fdividef(c0[i], 1.0f + __expf(-c0[i])) * c1[i];
+                    top = fmaxf(top, fabsf(c0[i]));
+                }
             }
             ctl->top[parity][half][row] = top;
             epi_bar();
@@ -416,64 +644,60 @@ __device__ void epilogue(unsigned char *out_stage, Ctl *ctl, const ProductArgs &
                 for (int i = 0; i < 16; ++i)
                     w[i] = pack_e4m3(c0[4 * i] * inv, c0[4 * i + 1] * inv, c0[4 * i + 2] * inv, c0[4 * i + 3] * inv);
                 const int f = x.nb * BLK + half * 64;
-                const size_t at = static_cast<size_t>(x.p0 + quarter * 32);
-                store_chunk(stage, o, reinterpret_cast<char *>(a.hq) + at * a.rows + f, a.rows, rows_here, lane,
-                            a.rows - f);
-                if (row < x.n && half == 0) a.hs[static_cast<size_t>(p) * rb + x.nb] = __int_as_float((127 + e) << 23);
-                if (x.nb == 0 && half == 0 && a.cnt != nullptr && row < x.n) {
-                    const int c = atomicAdd(a.cnt + ar, 1);  // by_pair is 0: ar is the entry's token
-                    if (c < a.k) a.inv[static_cast<size_t>(ar) * a.k + c] = p;
-                    else atomicCAS(a.error, 0, DEV_BAD_LISTS);
+                store_chunk(stage, o, reinterpret_cast<char *>(ph.hq) + row0 * ph.rows + f, ph.rows, rows_here, lane,
+                            ph.rows - f);
+                if (row < x.n && half == 0) {
+                    const int p = x.p0 + row;
+                    ph.hs[static_cast<size_t>(x.nb) * a.B * a.k + p] = __int_as_float((127 + e) << 23);
+                    if (x.nb == 0) {
+                        const int t = __ldg(a.tok + p);
+                        if (t >= 0 && t < a.B) {
+                            const int c = atomicAdd(a.cnt + t, 1);
+                            if (c < a.k) a.inv[static_cast<size_t>(t) * a.k + c] = p;
+                            else atomicCAS(a.error, 0, DEV_BAD_LISTS);
+                        }
+                    }
                 }
             }
+            // h and its scales are in memory, for the copies of any CTA, before the tile counts as done
+            fence_async();
+            __threadfence();
+            epi_bar();
+            if (threadIdx.x == 0 && !dead) add_release(a.done + x.mt);
         } else if (live && !dead) {
-            const size_t at = static_cast<size_t>(x.p0 + quarter * 32) * a.rows;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float(&c)[64] = m == 0 ? c0 : c1;
-                const int n0 = x.nb * TILE_N + m * BLK + half * 64;
-                uint4 o[4];
-                unsigned *w = reinterpret_cast<unsigned *>(o);
-                if (a.out_bf16) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(c[q * 32 + 2 * i], c[q * 32 + 2 * i + 1]);
-                        store_chunk(stage, o, static_cast<char *>(a.out) + (at + n0 + q * 32) * 2,
-                                    static_cast<size_t>(a.rows) * 2, rows_here, lane, (a.rows - n0 - q * 32) * 2);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(c[q * 16 + i]);
-                        store_chunk(stage, o, static_cast<char *>(a.out) + (at + n0 + q * 16) * 4,
-                                    static_cast<size_t>(a.rows) * 4, rows_here, lane, (a.rows - n0 - q * 16) * 4);
-                    }
-                }
-            }
+            const int n0 = x.nb * TILE_N + half * 64;
+            store_out(stage, c0, ph, row0, n0, rows_here, lane);
+            store_out(stage, c1, ph, row0, n0 + BLK, rows_here, lane);
         }
     }
 }
 
+template <int AR>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductMaps maps,
                                                              const __grid_constant__ ProductArgs a) {
+    using R = Ring<AR>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *out_stage = ring + STAGES * STAGE;
-    Ctl *ctl = reinterpret_cast<Ctl *>(out_stage + EPI_WARPS * OUT_STAGE);
+    unsigned char *out_stage = ring + R::STAGES * R::STAGE;
+    Ctl *ctl = reinterpret_cast<Ctl *>(out_stage + R::OUT_STAGES * OUT_STAGE);
     const int warp = threadIdx.x >> 5;
-    const int kb = (a.K + BLK - 1) / BLK;
-    const int nbt = a.kind == PRODUCT_SWIGLU ? (a.rows + BLK - 1) / BLK : (a.rows + TILE_N - 1) / TILE_N;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            bar_init(&ctl->full[i], 1);
+        for (int i = 0; i < R::STAGES; ++i) {
+            bar_init(&ctl->full[i], 2);  // weights and rows
             bar_init(&ctl->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&ctl->part_full[i], 1);
             bar_init(&ctl->part_free[i], EPI_WARPS);
+        }
+        for (int i = 0; i < SCALES; ++i) {
+            bar_init(&ctl->scale_full[i], 32);
+            bar_init(&ctl->scale_free[i], EPI_WARPS);
+        }
+        for (int i = 0; i < TILES; ++i) {
+            bar_init(&ctl->tile_full[i], 1);
+            bar_init(&ctl->tile_free[i], EPI_WARPS + 3);
         }
         bar_init(&ctl->mma_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -481,20 +705,48 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     }
     if (warp == EPI_WARPS + 1) tmem_alloc(saddr(&ctl->tmem), 512);
     tc_fence_before();
-    build_slots(ctl, a, nbt);  // ends in a block barrier
+    build_slots(ctl, a);  // ends in a block barrier
     tc_fence_after();
-    if (warp < EPI_WARPS) epilogue(out_stage, ctl, a, nbt, kb);
-    else if (warp == EPI_WARPS) producer(ring, ctl, maps, a, nbt, kb);
-    else issuer(ring, ctl, a, kb);
+    if (warp < EPI_WARPS) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+        epilogue_role<AR>(out_stage, ctl, a);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+        if (warp == EPI_WARPS) {
+            if (elect_one()) ctl->fills[0] = weights_role<AR>(ring, ctl, maps, a);
+        } else if (warp == EPI_WARPS + 1) {
+            if (elect_one()) {
+                issue_role<AR>(ring, ctl, a);
+                umma_commit(saddr(&ctl->mma_done));
+                const unsigned long long t0 = cycles();
+                while (!bar_try(&ctl->mma_done, 0) && cycles() - t0 < DRAIN_CYCLES) {
+                }
+            }
+        } else if (warp == EPI_WARPS + 2) {
+            const unsigned n = rows_role<AR>(ring, ctl, maps, a);
+            if ((threadIdx.x & 31) == 0) ctl->fills[1] = n;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (elect_one()) {
+            scheduler(ctl, a);
+        }
+        __syncwarp();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == EPI_WARPS + 1) tmem_dealloc(ctl->tmem, 512);
+    if (threadIdx.x == 0) {
+        drain_fills<R::STAGES>(ctl);
+        __threadfence();
+        if (atomicAdd(a.exits, 1) == static_cast<int>(gridDim.x) - 1) {
+            *a.next_tile = 0;
+            *a.exits = 0;
+        }
+    }
 }
 
-}  // namespace
-
-cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
+template <int AR>
+cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
     // per device: the SM count, and the shared-memory attribute set
     static int sms[MAX_DEVICES] = {};
     int dev = 0;
@@ -505,12 +757,20 @@ cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaSt
         int n = 0;
         err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (err != cudaSuccess) return err;
-        err = cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        err = cudaFuncSetAttribute(product_kernel<AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<AR>());
         if (err != cudaSuccess) return err;
         sms[dev] = n;
     }
-    product_kernel<<<sms[dev], THREADS, SMEM_BYTES, s>>>(maps, a);
+    product_kernel<AR><<<sms[dev], THREADS, smem_bytes<AR>(), s>>>(maps, a);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+int product_box_rows(int B) { return B <= 64 ? 64 : TILE_M; }
+
+cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
+    return a.B <= 64 ? launch_ar<64>(maps, a, s) : launch_ar<128>(maps, a, s);
 }
 
 }  // namespace moe

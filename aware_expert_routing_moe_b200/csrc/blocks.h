@@ -17,49 +17,71 @@ inline int blocks_of(int n) { return (n + BLK - 1) / BLK; }
 // error word first (moe_check_error), then what a call counts in.
 struct BlocksControl {
     int32_t error;
-    int32_t pad[63];
+    int32_t next_tile, exits;  // product kernel: tiles claimed, CTAs finished (zero between calls)
+    int32_t pad[61];
 };
 static_assert(sizeof(BlocksControl) <= MOE_GEMM_WORKSPACE_BYTES, "control segment does not fit");
 
+// Batches above DISPATCH_MIN tokens have each list entry's activation row
+// copied to its place in the lists, so that a tile's rows are one box; up to
+// it the rows are gathered by token.
+constexpr int DISPATCH_MIN = 64;
+
 struct BlocksWs {
-    size_t xq, xs, hq, hs, yp, cnt, inv, total;
+    size_t xq, xs, hq, hs, yp, counts, inv, total;
+    size_t n_counts;  // cnt [B], then done [m-tiles]
 };
 BlocksWs blocks_ws(const moe_dims_t &d);
 size_t route_ws_bytes(const moe_dims_t &d);
 
-// TMA descriptors of one grouped product: activation rows (gathered four at
-// a time) and two weight maps [E][rows][K] with boxes of 128 rows x 128
-// bytes (the same matrix twice for a plain product).
-struct ProductMaps {
-    CUtensorMap a, b0, b1;
+// TMA descriptors of a product's phases: activation rows as boxes of one row
+// (gathered four at a time) and of product_box_rows rows, and two weight maps
+// [E][rows][K] with boxes of 128 rows x 128 bytes (the same matrix twice for
+// a plain product).
+struct PhaseMaps {
+    CUtensorMap a, ab, b0, b1;
 };
-bool encode_product_maps(ProductMaps *m, const void *a, uint64_t a_rows, const void *b0, const void *b1,
-                         uint64_t E, uint64_t rows, uint64_t K);
+struct ProductMaps {
+    PhaseMaps phase[2];
+};
+int product_box_rows(int B);
+bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
+                       uint64_t E, uint64_t rows, uint64_t K);
 
 enum ProductKind : int { PRODUCT_OUT = 0, PRODUCT_SWIGLU = 1 };
 
-struct ProductArgs {
+struct ProductPhase {
     int kind;             // ProductKind
-    int B, E, k;          // dims of the lists
     int K, rows;          // columns of a weight row; rows of one weight matrix
     int by_pair;          // activation row of list entry p: p itself, else tok[p]
-    const float *as;      // activation scales [rows of a][blocks of K]
+    const float *as;      // activation scales: row r, block j at as[r * as_row + j * as_col]
+    int as_row, as_col;
     const float *bs0, *bs1;  // weight scales [E][blocks of rows][blocks of K]
-    const int32_t *n_active, *active, *offsets, *tok;
     void *out;            // PRODUCT_OUT: [entries][rows] fp32 or bf16
     int out_bf16;
     uint8_t *hq;          // PRODUCT_SWIGLU: [entries][rows] e4m3
-    float *hs;            // and its scales [entries][blocks of rows]
-    int32_t *cnt, *inv;   // entries of each token (or null): counts [B], entry indices [B][k]
-    int32_t *error;
+    float *hs;            // and its scales [blocks of rows][B * k]
+};
+struct ProductArgs {
+    ProductPhase phase[2];
+    int phases;
+    int B, E, k;          // dims of the lists
+    const int32_t *n_active, *active, *offsets, *tok;
+    int32_t *done;        // two phases: gate/up tiles done per m-tile
+    int32_t *cnt, *inv;   // two phases: entries of each token: counts [B], entry indices [B][k]
+    int32_t *error, *next_tile, *exits;
     unsigned long long wait_ns;
 };
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s);
 
 // e4m3 values and power-of-two scales of [batch][rows][cols] (block_rows 1
-// or 128); cnt (or null): B counters set to zero.
+// or 128).
 cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows, int64_t cols, int block_rows,
-                            uint8_t *q, float *scale, int32_t *cnt, int n_cnt, cudaStream_t s);
+                            uint8_t *q, float *scale, cudaStream_t s);
+// Rows of x [n_src][cols] (row src[r] when src is given; negative: skipped)
+// -> q [rows][cols], scales [blocks][rows]; zero[0 .. n_zero) = 0.
+cudaError_t launch_quantize_dispatch(const void *x, int type, int64_t rows, int cols, const int32_t *src, int n_src,
+                                     uint8_t *q, float *scale, int32_t *zero, int n_zero, cudaStream_t s);
 // y[t] = sum over the token's entries p, ascending, of w[p] * yp[p]
 cudaError_t launch_combine(const float *yp, const float *w, const int32_t *cnt, const int32_t *inv, int B, int d,
                            int k, void *y, int y_bf16, cudaStream_t s);

@@ -56,24 +56,32 @@ __device__ __forceinline__ unsigned abs_bits(const float4 &v) {
     return max(max(a, b), max(c, d));
 }
 
-// A warp per block of 128 columns: four columns a lane.
+// A warp per block of 128 columns: four columns a lane.  Scale of row r,
+// block j at scale[r * s_row + j * s_col].
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, long long rows, int cols, int cb,
+                                                            const int32_t *__restrict__ src, int n_src,
                                                             uint8_t *__restrict__ q, float *__restrict__ scale,
-                                                            int32_t *__restrict__ cnt, int n_cnt) {
+                                                            long long s_row, long long s_col,
+                                                            int32_t *__restrict__ zero, int n_zero) {
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * 8;
     const long long first = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (cnt != nullptr)
-        for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n_cnt; i += warps * 32) cnt[i] = 0;
+    if (zero != nullptr)
+        for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n_zero; i += warps * 32) zero[i] = 0;
     for (long long b = first; b < rows * cb; b += warps) {
         const long long r = b / cb;
-        const int c = static_cast<int>(b - r * cb) * BLK + lane * 4;
+        const int j = static_cast<int>(b - r * cb), c = j * BLK + lane * 4;
+        long long from = r;
+        if (src != nullptr) {
+            from = __ldg(src + r);
+            if (from < 0 || from >= n_src) continue;  // past the last entry (or a bad list, reported by the product)
+        }
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < cols) v = load4<T>(x + r * cols + c);
+        if (c < cols) v = load4<T>(x + from * cols + c);
         const int e = scale_exp(__reduce_max_sync(ALL, abs_bits(v)));
         if (c < cols) *reinterpret_cast<unsigned *>(q + r * cols + c) = pack4(v.x, v.y, v.z, v.w, pow2(-e));
-        if (lane == 0) scale[b] = pow2(e);
+        if (lane == 0) scale[r * s_row + j * s_col] = pow2(e);
     }
 }
 
@@ -155,20 +163,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 
 }  // namespace
 
+namespace {
+cudaError_t launch_rows(const void *x, int type, long long rows, int cols, const int32_t *src, int n_src, uint8_t *q,
+                        float *scale, long long s_row, long long s_col, int32_t *zero, int n_zero, cudaStream_t s) {
+    const int cb = blocks_of(cols);
+    const long long blocks = rows * cb;
+    const unsigned grid = static_cast<unsigned>(blocks + 7 < 8 * 148 * 16 ? (blocks + 7) / 8 : 148 * 16);
+    if (type == MOE_BF16)
+        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, cb, src, n_src, q,
+                                                  scale, s_row, s_col, zero, n_zero);
+    else
+        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), rows, cols, cb, src, n_src, q, scale,
+                                                  s_row, s_col, zero, n_zero);
+    return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_quantize_dispatch(const void *x, int type, int64_t rows, int cols, const int32_t *src, int n_src,
+                                     uint8_t *q, float *scale, int32_t *zero, int n_zero, cudaStream_t s) {
+    return launch_rows(x, type, rows, cols, src, n_src, q, scale, 1, rows, zero, n_zero, s);
+}
+
 cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows, int64_t cols, int block_rows,
-                            uint8_t *q, float *scale, int32_t *cnt, int n_cnt, cudaStream_t s) {
+                            uint8_t *q, float *scale, cudaStream_t s) {
     const int cb = blocks_of(static_cast<int>(cols)), c = static_cast<int>(cols);
-    if (block_rows == 1) {
-        const long long blocks = batch * rows * cb;
-        const unsigned grid = static_cast<unsigned>(blocks + 7 < 8 * 148 * 16 ? (blocks + 7) / 8 : 148 * 16);
-        if (type == MOE_BF16)
-            quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), batch * rows, c, cb, q,
-                                                      scale, cnt, n_cnt);
-        else
-            quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), batch * rows, c, cb, q, scale,
-                                                      cnt, n_cnt);
-        return cudaGetLastError();
-    }
+    if (block_rows == 1) return launch_rows(x, type, batch * rows, c, nullptr, 0, q, scale, cb, 1, nullptr, 0, s);
     const int rb = blocks_of(static_cast<int>(rows)), r = static_cast<int>(rows);
     const unsigned grid = static_cast<unsigned>(batch * rb * cb);
     if (type == MOE_BF16)

@@ -148,8 +148,10 @@ def ffn(x, weights, lists, B):
         eg, eu = (sum_bound(d, np.abs(a) @ np.abs(W[e]).T) for W in (Wg, Wu))
         z = 1.0 / (1.0 + np.exp(-g))
         h = g * z * u
-        # |d silu / dg| <= 1.1; exp, the division and two products round
-        eh = 1.1 * eg * np.abs(u) + np.abs(g * z) * eu + 1.1 * eg * eu + 8 * 2.0 ** -23 * np.abs(h)
+        # |d silu / dg| <= 1.1; exp, the division and two products round, and a
+        # fast exp(-g) = 2^(-g log2 e) also turns the rounding of its argument
+        # (|g| log2 e 2^-24) into a relative error of |g| 2^-24
+        eh = 1.1 * eg * np.abs(u) + np.abs(g * z) * eu + 1.1 * eg * eu + (8 + np.abs(g)) * 2.0 ** -23 * np.abs(h)
         hq, hs = quantize(h)
         n, F = h.shape
         full = spread(hs, n, F, 1)
