@@ -313,9 +313,9 @@ BlocksWs blocks_ws(const moe_dims_t &d) {
     size_t o = MOE_GEMM_WORKSPACE_BYTES;
     const size_t rows = d.B > DISPATCH_MIN ? P : B;  // quantised activation rows
     w.xq = o;  o += round_up(rows * D);
-    w.xs = o;  o += round_up(rows * blocks_of(d.d) * 4);
+    w.xs = o;  o += round_up(rows * scale_pitch(d.d) * 4);
     w.hq = o;  o += round_up(P * F);
-    w.hs = o;  o += round_up(P * blocks_of(d.d_ff) * 4);
+    w.hs = o;  o += round_up(P * scale_pitch(d.d_ff) * 4);
     w.yp = o;  o += round_up(P * D * 4);
     // m-tiles: one per 128 entries, and a short one per active expert at most
     w.n_counts = B + (P / 128 + (E < P ? E : P));
@@ -611,8 +611,7 @@ moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const 
     p.K = dims.d;
     p.rows = dims.d_ff;
     p.as = scale;
-    p.as_row = blocks_of(dims.d);
-    p.as_col = 1;
+    p.as_pitch = blocks_of(dims.d);
     p.bs0 = p.bs1 = Wscale;
     p.out = y;
     p.out_bf16 = y_type == MOE_BF16;
@@ -660,19 +659,18 @@ moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weig
     up.rows = dims.d_ff;
     up.by_pair = dispatch;
     up.as = xs;
-    up.as_row = 1;
-    up.as_col = rows;
+    up.as_pitch = scale_pitch(dims.d);
     up.bs0 = w.Sgate;
     up.bs1 = w.Sup;
     up.hq = hq;
     up.hs = hs;
+    up.hs_pitch = scale_pitch(dims.d_ff);
     down.kind = PRODUCT_OUT;
     down.K = dims.d_ff;
     down.rows = dims.d;
     down.by_pair = 1;
     down.as = hs;
-    down.as_row = 1;
-    down.as_col = pairs;
+    down.as_pitch = scale_pitch(dims.d_ff);
     down.bs0 = down.bs1 = w.Sdown;
     down.out = yp;
     st = from_cuda(launch_quantize_dispatch(x, x_type, rows, dims.d, dispatch ? lists.tok : nullptr, dims.B, xq, xs,

@@ -25,7 +25,8 @@
 // the tile's activations); warp 9 MMAs; warp 10 activation rows (a box, or
 // gathered four at a time by list entry) and the scales of each column
 // block, copied to a ring of their own, so that no global load latency sits
-// in the epilogue's loop; warp 11 claims tiles.  Every wait is bounded; past
+// in the epilogue's loop; warp 11 claims tiles and
+// publishes finished ones.  Every wait is bounded; past
 // the limit the CTA records an error, lets its copies and MMAs land and
 // leaves.
 #include <cuda_bf16.h>
@@ -48,7 +49,8 @@ constexpr int REGS_EPI = 224, REGS_COPY = 56;
 static_assert(256 * REGS_EPI + 128 * REGS_COPY <= THREADS * 168, "register split");
 constexpr int OUT_PITCH = 80;     // bytes of a staged output row: 64 and a pad that spreads the banks
 constexpr int OUT_STAGE = 32 * OUT_PITCH;
-constexpr int SCALES = 8;         // column blocks whose scales are in flight
+constexpr int SGROUP = 4;         // column blocks whose scales are copied together (16 bytes a row)
+constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
 constexpr int GATHER_MAX = 32;    // rows that are gathered although they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
@@ -66,6 +68,7 @@ struct Ring {
 enum : int { TILE_END = 2 };
 struct Tile {
     int phase, e, p0, n, nb, mt;  // phase (TILE_END: no more), expert, first entry, entries, column tile, m-tile
+    int ready;                    // down: its gate/up tiles were done when it was claimed
 };
 
 struct Ctl {
@@ -73,20 +76,26 @@ struct Ctl {
     unsigned long long part_full[2], part_free[2];
     unsigned long long scale_full[SCALES], scale_free[SCALES];
     unsigned long long tile_full[TILES], tile_free[TILES];
+    unsigned long long pub_full[2], pub_free[2];
     unsigned long long mma_done;
     volatile int abort_flag;
     int n_slots, m_tiles;
     unsigned fills[2];  // stages filled with weights, with rows
     uint32_t tmem;
     Tile tile[TILES];
-    float scale[SCALES][TILE_M + 4];  // 128 row scales, then the two weight blocks'
-    float top[2][2][TILE_M];          // [tile parity][column half][row]: largest |h|
-    int act[SE_MAX], off[SE_MAX + 1], mt[SE_MAX + 1];  // expert, first entry, first m-tile of a slot
+    int rows[TILES][TILE_M];          // activation row of each entry of a claimed tile
+    int pub_mt[2];                    // m-tile of a finished gate/up tile
+    float4 scale[SCALES][TILE_M];     // each row's scales of a group of column blocks
+    float wscale[SCALES][2][SGROUP];  // and the two weight blocks'
+    float top[2][TILE_M];             // [column half][row]: largest |h|
+    int off[SE_MAX + 1];              // first entry of a slot, its first m-tile, its expert
+    uint16_t mt[SE_MAX + 1], act[SE_MAX];
 };
 template <int AR>
 constexpr int smem_bytes() {
     return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_STAGES * OUT_STAGE + static_cast<int>(sizeof(Ctl));
 }
+static_assert(ST_MAX * K_MAX / TILE_M + SE_MAX < 65536, "m-tile numbers are 16 bits");
 static_assert(smem_bytes<128>() <= 232448 - 64 && smem_bytes<64>() <= 232448 - 64, "shared memory budget");
 // an MMA reads 128 activation rows: those past a 64-row region are bytes of
 // the next region (their sums are not used)
@@ -107,6 +116,9 @@ __device__ __forceinline__ void bar_expect(unsigned long long *b, unsigned bytes
 }
 __device__ __forceinline__ void bar_arrive(unsigned long long *b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr(dst)), "l"(src) : "memory");
 }
 // four bytes global -> shared; arrive on b when this thread's copies land
 __device__ __forceinline__ void copy4(void *dst, const void *src) {
@@ -190,19 +202,29 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t adesc, uint64_t b
         "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
         : "memory");
 }
-// 32 consecutive fp32 columns of the warp's 32 TMEM lanes
+// 32 consecutive fp32 columns of the warp's 32 TMEM lanes; the registers
+// hold them after tmem_wait, which also waits for the loads issued before
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 // Bounded wait on an mbarrier phase; false once the CTA has given up.
@@ -267,7 +289,7 @@ __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
         bool bad = o < 0 || o > a.B * a.k || (i == 0 && n > 0 && o != 0);
         if (i < n) {
             const int e = __ldg(a.active + i), next = __ldg(a.offsets + i + 1);
-            ctl->act[i] = e;
+            ctl->act[i] = static_cast<uint16_t>(e);
             bad = bad || e < 0 || e >= a.E || next < o || next - o > a.B;
         }
         if (bad) s_bad = 1;
@@ -285,11 +307,11 @@ __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
                 const int u = __shfl_up_sync(ALL, v, o);
                 if (static_cast<int>(threadIdx.x) >= o) v += u;
             }
-            if (i < n) ctl->mt[i] = run + v - mine;
+            if (i < n) ctl->mt[i] = static_cast<uint16_t>(run + v - mine);
             run += __shfl_sync(ALL, v, 31);
         }
         if (threadIdx.x == 0) {
-            ctl->mt[n] = run;
+            ctl->mt[n] = static_cast<uint16_t>(run);
             ctl->n_slots = n;
             ctl->m_tiles = run;
             if (s_bad && blockIdx.x == 0) atomicCAS(a.error, 0, DEV_BAD_LISTS);
@@ -318,20 +340,98 @@ struct TileCursor {
 };
 
 // --------------------------------------------------------------- roles --
+// Claims tiles ahead of the other roles (with the activation rows of their
+// entries), and publishes finished gate/up tiles: the fence before a
+// publication takes a microsecond that the epilogue does not wait for.
 __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
+    const int lane = threadIdx.x & 31;
     const int nbt0 = column_tiles(a.phase[0]), t0 = ctl->m_tiles * nbt0;
     const int nbt1 = a.phases > 1 ? column_tiles(a.phase[1]) : 0, total = t0 + ctl->m_tiles * nbt1;
-    for (unsigned i = 0;; ++i) {
-        const int s = i % TILES;
-        if (i >= TILES && !wait_bar(&ctl->tile_free[s], (i / TILES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY)) return;
-        const int t = atomicAdd(a.next_tile, 1);
-        Tile x;
-        x.phase = TILE_END;
-        if (t < t0) x = tile_at(t, 0, nbt0, ctl);
-        else if (t < total) x = tile_at(t - t0, 1, nbt1, ctl);
-        ctl->tile[s] = x;
-        bar_arrive(&ctl->tile_full[s]);
-        if (x.phase == TILE_END) return;
+    unsigned claimed = 0, published = 0, to_publish = 0;
+    bool open = true, waited = false;
+    unsigned long long since = cycles();
+    while (open || published < to_publish) {
+        bool idle = true;
+        const int s = claimed % TILES;
+        bool slot = false;
+        if (open) slot = __all_sync(ALL, claimed < TILES || bar_try(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
+        if (slot) {
+            int t = 0;
+            if (lane == 0) t = atomicAdd(a.next_tile, 1);
+            t = __shfl_sync(ALL, t, 0);
+            Tile x;
+            x.phase = TILE_END;
+            x.n = x.ready = 0;
+            if (t < t0) x = tile_at(t, 0, nbt0, ctl);
+            else if (t < total) x = tile_at(t - t0, 1, nbt1, ctl);
+            int tok[4];
+            if (x.phase != TILE_END) {
+                const bool by_pair = a.phase[x.phase].by_pair != 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // rows past the tile's end repeat its last one (their sums are not used)
+                    const int p = x.p0 + min(lane + 32 * q, x.n - 1);
+                    int r = p;
+                    if (!by_pair || x.phase == 0) {
+                        tok[q] = __ldg(a.tok + p);
+                        if (tok[q] < 0 || tok[q] >= a.B) {
+                            atomicCAS(a.error, 0, DEV_BAD_LISTS);
+                            tok[q] = -1;
+                        }
+                        if (!by_pair) r = max(tok[q], 0);
+                    }
+                    ctl->rows[s][lane + 32 * q] = r;
+                }
+                if (x.phase == 1) {
+                    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are zero
+                    waited = true;
+                    x.ready = ld_acquire(a.done + x.mt) >= nbt0;
+                }
+            }
+            if (lane == 0) ctl->tile[s] = x;
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ctl->tile_full[s]);
+            ++claimed;
+            open = x.phase != TILE_END;
+            if (a.phases > 1 && x.phase == 0) {
+                ++to_publish;
+                if (x.nb == 0) {  // the entries of each token, for the combine
+                    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                    waited = true;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int p = x.p0 + lane + 32 * q;
+                        if (lane + 32 * q >= x.n || tok[q] < 0) continue;
+                        const int c = atomicAdd(a.cnt + tok[q], 1);
+                        if (c < a.k) a.inv[static_cast<size_t>(tok[q]) * a.k + c] = p;
+                        else atomicCAS(a.error, 0, DEV_BAD_LISTS);
+                    }
+                }
+            }
+            idle = false;
+        }
+        if (published < to_publish && __all_sync(ALL, bar_try(&ctl->pub_full[published & 1], (published >> 1) & 1))) {
+            if (lane == 0) {
+                const int mt = ctl->pub_mt[published & 1];
+                // h and its scales, written by the epilogue's threads, are in
+                // memory for the copies of any CTA before the tile counts
+                fence_async();
+                __threadfence();
+                add_release(a.done + mt);
+                bar_arrive(&ctl->pub_free[published & 1]);
+            }
+            __syncwarp();
+            ++published;
+            idle = false;
+        }
+        if (!idle) since = cycles();
+        else if (__any_sync(ALL, ctl->abort_flag || cycles() - since > a.wait_ns * CYCLES_PER_NS)) {
+            if (lane == 0 && !ctl->abort_flag) {
+                atomicCAS(a.error, 0, DEV_TIMEOUT_EMPTY);
+                ctl->abort_flag = 1;
+            }
+            return;
+        }
     }
 }
 
@@ -365,7 +465,8 @@ __device__ unsigned weights_role(unsigned char *ring, Ctl *ctl, const ProductMap
         for (int j = 0; j < kb; ++j, ++it) {
             const int st = it % R::STAGES;
             unsigned char *w = ring + st * R::STAGE;
-            if (it >= R::STAGES && !wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY)) return it;
+            if (it >= R::STAGES && !wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY))
+                return it;
             bar_expect(&ctl->full[st], W_STAGE);
             load_box(w, m0, j * BLK, r0, x.e, &ctl->full[st]);
             load_box(w + W_STAGE / 2, m1, j * BLK, r1, x.e, &ctl->full[st]);
@@ -380,9 +481,19 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
     const int lane = threadIdx.x & 31;
     TileCursor cur;
     Tile x;
-    unsigned it = 0;
+    unsigned it = 0, sg = 0;
+    int st = 0;
+    unsigned phase = 0;  // of stage st's present fill
+    // the activations are the previous kernel's
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (;;) {
         if (!__all_sync(ALL, cur.next(ctl, a, x))) return it;
+        int rows[4], srow[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            rows[q] = ctl->rows[cur.i % TILES][lane * 4 + q];
+            srow[q] = ctl->rows[cur.i % TILES][lane + 32 * q];
+        }
         __syncwarp();
         if (lane == 0) cur.release(ctl);
         else ++cur.i;
@@ -391,52 +502,30 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
         const int kb = (ph.K + BLK - 1) / BLK, rb = (ph.rows + BLK - 1) / BLK;
         if (x.phase == 1) {
             // the entries' gate/up tiles are all done
-            const int need = column_tiles(a.phase[0]);
             bool ok = true;
-            if (lane == 0 && ld_acquire(a.done + x.mt) < need) {
+            if (lane == 0 && !x.ready) {
+                const int need = column_tiles(a.phase[0]);
                 const unsigned long long t0 = cycles();
-                while (ld_acquire(a.done + x.mt) < need) {
+                while (ok && ld_acquire(a.done + x.mt) < need) {
                     ok = !ctl->abort_flag;
                     if (ok && cycles() - t0 > a.wait_ns * CYCLES_PER_NS) {
                         atomicCAS(a.error, 0, DEV_TIMEOUT_DEP);
                         ctl->abort_flag = 1;
                         ok = false;
                     }
-                    if (!ok) break;
                 }
             }
             if (!__all_sync(ALL, ok)) return it;
             fence_async();
         }
         // lane l copies the scales of rows l, l + 32, ..., and gathers rows 4 l ..
-        const int last = (ph.by_pair ? a.B * a.k : a.B) - 1;
         const float *src[4];
-        int rows[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            // rows past the tile's end repeat its last one (their sums are not used)
-            const int p = x.p0 + min(lane * 4 + q, x.n - 1), ps = x.p0 + min(lane + 32 * q, x.n - 1);
-            int r = p, rs = ps;
-            if (!ph.by_pair) {
-                r = __ldg(a.tok + p);
-                rs = __ldg(a.tok + ps);
-                if (r < 0 || r > last) {
-                    atomicCAS(a.error, 0, DEV_BAD_LISTS);
-                    r = 0;
-                }
-                if (rs < 0 || rs > last) rs = 0;
-            }
-            rows[q] = r;
-            src[q] = ph.as + rs * static_cast<size_t>(ph.as_row);
-        }
-        const float *wsrc = nullptr;
-        if (lane == 0) {
-            const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : 2 * x.nb;
-            wsrc = ph.bs0 + (static_cast<size_t>(x.e) * rb + nb) * kb;
-        } else if (lane == 1) {
-            const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + 1, rb - 1);
-            wsrc = ph.bs1 + (static_cast<size_t>(x.e) * rb + nb) * kb;
-        }
+        for (int q = 0; q < 4; ++q) src[q] = ph.as + srow[q] * static_cast<size_t>(ph.as_pitch);
+        // lanes 0-3 and 4-7: a group's scales of the two weight blocks
+        const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + (lane >> 2), rb - 1);
+        const float *wsrc = (lane < 4 ? ph.bs0 : ph.bs1) + (static_cast<size_t>(x.e) * rb + nb) * kb;
+        const bool wide = (ph.as_pitch & 3) == 0;
         // consecutive rows in one box; few rows, or scattered ones, four at a time
         const int first = __shfl_sync(ALL, rows[0], 0);
         bool run = true;
@@ -446,23 +535,39 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
         const int groups = (x.n + 3) >> 2;
         const unsigned bytes = box ? R::A_STAGE : groups * 4 * BLK;
         const CUtensorMap *m = box ? &maps.phase[x.phase].ab : &maps.phase[x.phase].a;
-        for (int j = 0; j < kb; ++j, ++it) {
-            const int st = it % R::STAGES, sc = it % SCALES;
-            unsigned char *d = ring + st * R::STAGE + W_STAGE;
-            bool ok = it < R::STAGES || wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY);
-            ok = ok && (it < SCALES || wait_bar(&ctl->scale_free[sc], (it / SCALES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY));
-            if (!__all_sync(ALL, ok)) return it;
-            if (lane == 0) {
-                bar_expect(&ctl->full[st], bytes);
-                if (box) load_rows(d, m, j * BLK, first, &ctl->full[st]);
-            }
-            __syncwarp();
-            if (!box && lane < groups) load_rows4(d + lane * 4 * BLK, m, j * BLK, rows, &ctl->full[st]);
+        const bool mine = box ? lane == 0 : lane < groups;
+        for (int j = 0; j < kb; ++j) {
+            if (j % SGROUP == 0) {
+                const unsigned sc = sg % SCALES;
+                if (sg >= SCALES && !__all_sync(ALL, wait_bar(&ctl->scale_free[sc], (sg / SCALES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY)))
+                    return it;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (lane + 32 * q < x.n) copy4(&ctl->scale[sc][lane + 32 * q], src[q] + static_cast<size_t>(j) * ph.as_col);
-            if (lane < 2) copy4(&ctl->scale[sc][TILE_M + lane], wsrc + j);
-            copies_arrive(&ctl->scale_full[sc]);
+                for (int q = 0; q < 4; ++q) {
+                    const int r = lane + 32 * q;
+                    if (r >= x.n) break;
+                    if (wide) copy16(&ctl->scale[sc][r], src[q] + j);
+                    else
+                        for (int i = 0; i < SGROUP && j + i < kb; ++i)
+                            copy4(reinterpret_cast<float *>(&ctl->scale[sc][r]) + i, src[q] + j + i);
+                }
+                if (lane < 8 && j + (lane & 3) < kb) copy4(&ctl->wscale[sc][lane >> 2][lane & 3], wsrc + j + (lane & 3));
+                copies_arrive(&ctl->scale_full[sc]);
+                ++sg;
+            }
+            unsigned long long *full = &ctl->full[st];
+            if (it >= R::STAGES && !__all_sync(ALL, wait_bar(&ctl->empty[st], phase ^ 1, ctl, a, DEV_TIMEOUT_EMPTY))) return it;
+            if (lane == 0) bar_expect(full, bytes);
+            __syncwarp();
+            if (mine) {
+                unsigned char *d = ring + st * R::STAGE + W_STAGE;
+                if (box) load_rows(d, m, j * BLK, first, full);
+                else load_rows4(d + lane * 4 * BLK, m, j * BLK, rows, full);
+            }
+            ++it;
+            if (++st == R::STAGES) {
+                st = 0;
+                phase ^= 1;
+            }
         }
     }
 }
@@ -527,6 +632,12 @@ __device__ __forceinline__ void store_chunk(unsigned char *stage, const uint4 (&
     __syncwarp();
 }
 
+// c[0 .. 32) += v * m
+__device__ __forceinline__ void add32(float *c, const uint32_t (&v)[32], float m) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) fma2(c[i], c[i + 1], v[i], v[i + 1], m);
+}
+
 __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d) {
     unsigned short lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -571,14 +682,13 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
     const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
     unsigned char *stage = out_stage + (half * (AR / 32) + quarter) * OUT_STAGE;  // used by warps with rows
     bool dead = false;
-    unsigned it = 0;
+    unsigned it = 0, gu = 0, sg = 0;
     TileCursor cur;
     Tile x;
     for (;;) {
         dead = dead || !cur.next(ctl, a, x);
         if (epi_any(dead)) return;  // together, so that none is left at a barrier
         __syncwarp();
-        const int parity = cur.i & 1;
         if (lane == 0) cur.release(ctl);
         else ++cur.i;
         if (x.phase == TILE_END) return;
@@ -589,32 +699,47 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
 #pragma unroll
         for (int i = 0; i < 64; ++i) c0[i] = c1[i] = 0.0f;
         for (int j = 0; j < kb; ++j, ++it) {
-            const int buf = it & 1, sc = it % SCALES;
-            bool ok = !dead && wait_bar(&ctl->scale_full[sc], (it / SCALES) & 1, ctl, a, DEV_TIMEOUT_FULL);
+            const int buf = it & 1, sc = sg % SCALES;
+            bool ok = !dead;
+            if (j % SGROUP == 0) ok = ok && wait_bar(&ctl->scale_full[sc], (sg / SCALES) & 1, ctl, a, DEV_TIMEOUT_FULL);
             ok = ok && wait_bar(&ctl->part_full[buf], (it >> 1) & 1, ctl, a, DEV_TIMEOUT_FULL);
             dead = !__all_sync(ALL, ok);
+            const bool last = j % SGROUP == SGROUP - 1 || j + 1 == kb;  // of the group
+            sg += last;
             if (dead) continue;
             tc_fence_after();
             if (live) {
-                const float fa = ctl->scale[sc][row];
-                const float m0 = fa * ctl->scale[sc][TILE_M], m1 = fa * ctl->scale[sc][TILE_M + 1];
                 const uint32_t col = tbase + buf * TILE_N;
-                uint32_t v[32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    tmem_ld32(col + q * 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) fma2(c0[q * 32 + i], c0[q * 32 + i + 1], v[i], v[i + 1], m0);
-                    tmem_ld32(col + 128 + q * 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) fma2(c1[q * 32 + i], c1[q * 32 + i + 1], v[i], v[i + 1], m1);
+                // a load is in flight while the one before is added; the
+                // buffer goes back to the MMAs before the last additions
+                uint32_t u[32], v[32];
+                tmem_ld32(col, u);
+                const float f = reinterpret_cast<const float *>(&ctl->scale[sc][row])[j % SGROUP];
+                const float m0 = f * ctl->wscale[sc][0][j % SGROUP], m1 = f * ctl->wscale[sc][1][j % SGROUP];
+                tmem_wait(u);
+                tmem_ld32(col + 32, v);
+                add32(c0, u, m0);
+                tmem_wait(v);
+                tmem_ld32(col + 128, u);
+                add32(c0 + 32, v, m0);
+                tmem_wait(u);
+                tmem_ld32(col + 160, v);
+                add32(c1, u, m1);
+                tmem_wait(v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(&ctl->part_free[buf]);
+                    if (last) bar_arrive(&ctl->scale_free[sc]);
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                bar_arrive(&ctl->part_free[buf]);
-                bar_arrive(&ctl->scale_free[sc]);
+                add32(c1 + 32, v, m1);
+            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(&ctl->part_free[buf]);
+                    if (last) bar_arrive(&ctl->scale_free[sc]);
+                }
             }
         }
         const int rows_here = min(32, x.n - quarter * 32);
@@ -630,10 +755,11 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                     top = fmaxf(top, fabsf(c0[i]));
                 }
             }
-            ctl->top[parity][half][row] = top;
+            // (read again only after the next tile's meeting)
+            ctl->top[half][row] = top;
             epi_bar();
             if (live && !dead) {
-                top = fmaxf(ctl->top[parity][0][row], ctl->top[parity][1][row]);
+                top = fmaxf(ctl->top[0][row], ctl->top[1][row]);
                 const unsigned tb = __float_as_uint(top);
                 int e = tb == 0u ? 0 : static_cast<int>(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
                 e = e < -120 ? -120 : e;
@@ -646,24 +772,15 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                 const int f = x.nb * BLK + half * 64;
                 store_chunk(stage, o, reinterpret_cast<char *>(ph.hq) + row0 * ph.rows + f, ph.rows, rows_here, lane,
                             ph.rows - f);
-                if (row < x.n && half == 0) {
-                    const int p = x.p0 + row;
-                    ph.hs[static_cast<size_t>(x.nb) * a.B * a.k + p] = __int_as_float((127 + e) << 23);
-                    if (x.nb == 0) {
-                        const int t = __ldg(a.tok + p);
-                        if (t >= 0 && t < a.B) {
-                            const int c = atomicAdd(a.cnt + t, 1);
-                            if (c < a.k) a.inv[static_cast<size_t>(t) * a.k + c] = p;
-                            else atomicCAS(a.error, 0, DEV_BAD_LISTS);
-                        }
-                    }
-                }
+                if (row < x.n && half == 0)
+                    ph.hs[static_cast<size_t>(x.p0 + row) * ph.hs_pitch + x.nb] = __int_as_float((127 + e) << 23);
             }
-            // h and its scales are in memory, for the copies of any CTA, before the tile counts as done
-            fence_async();
-            __threadfence();
-            epi_bar();
-            if (threadIdx.x == 0 && !dead) add_release(a.done + x.mt);
+            const int slot = gu & 1;
+            if (gu >= 2 && !dead) dead = !__all_sync(ALL, wait_bar(&ctl->pub_free[slot], ((gu >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP));
+            ++gu;
+            if (threadIdx.x == 0) ctl->pub_mt[slot] = x.mt;
+            __syncwarp();
+            if (lane == 0 && !dead) bar_arrive(&ctl->pub_full[slot]);
         } else if (live && !dead) {
             const int n0 = x.nb * TILE_N + half * 64;
             store_out(stage, c0, ph, row0, n0, rows_here, lane);
@@ -699,10 +816,15 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             bar_init(&ctl->tile_full[i], 1);
             bar_init(&ctl->tile_free[i], EPI_WARPS + 3);
         }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ctl->pub_full[i], EPI_WARPS);
+            bar_init(&ctl->pub_free[i], 1);
+        }
         bar_init(&ctl->mma_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ctl->abort_flag = 0;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == EPI_WARPS + 1) tmem_alloc(saddr(&ctl->tmem), 512);
     tc_fence_before();
     build_slots(ctl, a);  // ends in a block barrier
@@ -726,7 +848,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             const unsigned n = rows_role<AR>(ring, ctl, maps, a);
             if ((threadIdx.x & 31) == 0) ctl->fills[1] = n;
             asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (elect_one()) {
+        } else {
             scheduler(ctl, a);
         }
         __syncwarp();
@@ -761,8 +883,18 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
         if (err != cudaSuccess) return err;
         sms[dev] = n;
     }
-    product_kernel<AR><<<sms[dev], THREADS, smem_bytes<AR>(), s>>>(maps, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms[dev]);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<AR>();
+    cfg.stream = s;
+    // after the quantisation kernel: claim tiles and stream weights meanwhile
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.phases > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, product_kernel<AR>, maps, a);
 }
 
 }  // namespace

@@ -12,6 +12,9 @@ constexpr int ST_MAX = 65536;        // tokens
 constexpr int SD_MIN = 16, SD_MAX = 16384;
 
 inline int blocks_of(int n) { return (n + BLK - 1) / BLK; }
+// floats between the scales of two rows in the library's own buffers: whole
+// 16-byte pieces, which one copy each moves
+inline int scale_pitch(int cols) { return (blocks_of(cols) + 3) / 4 * 4; }
 
 // Control segment at the start of every workspace of these operators: the
 // error word first (moe_check_error), then what a call counts in.
@@ -54,13 +57,14 @@ struct ProductPhase {
     int kind;             // ProductKind
     int K, rows;          // columns of a weight row; rows of one weight matrix
     int by_pair;          // activation row of list entry p: p itself, else tok[p]
-    const float *as;      // activation scales: row r, block j at as[r * as_row + j * as_col]
-    int as_row, as_col;
+    const float *as;      // activation scales: row r, block j at as[r * as_pitch + j]
+    int as_pitch;
     const float *bs0, *bs1;  // weight scales [E][blocks of rows][blocks of K]
     void *out;            // PRODUCT_OUT: [entries][rows] fp32 or bf16
     int out_bf16;
     uint8_t *hq;          // PRODUCT_SWIGLU: [entries][rows] e4m3
-    float *hs;            // and its scales [blocks of rows][B * k]
+    float *hs;            // and its scales, row p's block j at hs[p * hs_pitch + j]
+    int hs_pitch;
 };
 struct ProductArgs {
     ProductPhase phase[2];
@@ -79,7 +83,7 @@ cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaSt
 cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows, int64_t cols, int block_rows,
                             uint8_t *q, float *scale, cudaStream_t s);
 // Rows of x [n_src][cols] (row src[r] when src is given; negative: skipped)
-// -> q [rows][cols], scales [blocks][rows]; zero[0 .. n_zero) = 0.
+// -> q [rows][cols], scales [rows][scale_pitch(cols)]; zero[0 .. n_zero) = 0.
 cudaError_t launch_quantize_dispatch(const void *x, int type, int64_t rows, int cols, const int32_t *src, int n_src,
                                      uint8_t *q, float *scale, int32_t *zero, int n_zero, cudaStream_t s);
 // y[t] = sum over the token's entries p, ascending, of w[p] * yp[p]

@@ -57,13 +57,13 @@ __device__ __forceinline__ unsigned abs_bits(const float4 &v) {
 }
 
 // A warp per block of 128 columns: four columns a lane.  Scale of row r,
-// block j at scale[r * s_row + j * s_col].
+// block j at scale[r * pitch + j].
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, long long rows, int cols, int cb,
                                                             const int32_t *__restrict__ src, int n_src,
                                                             uint8_t *__restrict__ q, float *__restrict__ scale,
-                                                            long long s_row, long long s_col,
-                                                            int32_t *__restrict__ zero, int n_zero) {
+                                                            int pitch, int32_t *__restrict__ zero, int n_zero) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * 8;
     const long long first = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
         if (c < cols) v = load4<T>(x + from * cols + c);
         const int e = scale_exp(__reduce_max_sync(ALL, abs_bits(v)));
         if (c < cols) *reinterpret_cast<unsigned *>(q + r * cols + c) = pack4(v.x, v.y, v.z, v.w, pow2(-e));
-        if (lane == 0) scale[r * s_row + j * s_col] = pow2(e);
+        if (lane == 0) scale[r * pitch + j] = pow2(e);
     }
 }
 
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
                                                       void *__restrict__ y, int y_bf16) {
     __shared__ int s_p[K_MAX];
     __shared__ float s_w[K_MAX];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = blockIdx.x;
     const int n = min(cnt[t], k);
     if (threadIdx.x < n) {  // entries in ascending order
@@ -165,29 +166,29 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 
 namespace {
 cudaError_t launch_rows(const void *x, int type, long long rows, int cols, const int32_t *src, int n_src, uint8_t *q,
-                        float *scale, long long s_row, long long s_col, int32_t *zero, int n_zero, cudaStream_t s) {
+                        float *scale, int pitch, int32_t *zero, int n_zero, cudaStream_t s) {
     const int cb = blocks_of(cols);
     const long long blocks = rows * cb;
     const unsigned grid = static_cast<unsigned>(blocks + 7 < 8 * 148 * 16 ? (blocks + 7) / 8 : 148 * 16);
     if (type == MOE_BF16)
         quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, cb, src, n_src, q,
-                                                  scale, s_row, s_col, zero, n_zero);
+                                                  scale, pitch, zero, n_zero);
     else
         quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), rows, cols, cb, src, n_src, q, scale,
-                                                  s_row, s_col, zero, n_zero);
+                                                  pitch, zero, n_zero);
     return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_quantize_dispatch(const void *x, int type, int64_t rows, int cols, const int32_t *src, int n_src,
                                      uint8_t *q, float *scale, int32_t *zero, int n_zero, cudaStream_t s) {
-    return launch_rows(x, type, rows, cols, src, n_src, q, scale, 1, rows, zero, n_zero, s);
+    return launch_rows(x, type, rows, cols, src, n_src, q, scale, scale_pitch(cols), zero, n_zero, s);
 }
 
 cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows, int64_t cols, int block_rows,
                             uint8_t *q, float *scale, cudaStream_t s) {
     const int cb = blocks_of(static_cast<int>(cols)), c = static_cast<int>(cols);
-    if (block_rows == 1) return launch_rows(x, type, batch * rows, c, nullptr, 0, q, scale, cb, 1, nullptr, 0, s);
+    if (block_rows == 1) return launch_rows(x, type, batch * rows, c, nullptr, 0, q, scale, cb, nullptr, 0, s);
     const int rb = blocks_of(static_cast<int>(rows)), r = static_cast<int>(rows);
     const unsigned grid = static_cast<unsigned>(batch * rb * cb);
     if (type == MOE_BF16)
@@ -200,8 +201,16 @@ cudaError_t launch_quantize(const void *x, int type, int64_t batch, int64_t rows
 cudaError_t launch_combine(const float *yp, const float *w, const int32_t *cnt, const int32_t *inv, int B, int d,
                            int k, void *y, int y_bf16, cudaStream_t s) {
     const int threads = d >= 1024 ? 256 : 64;
-    combine_kernel<<<B, threads, 0, s>>>(yp, w, cnt, inv, d, k, y, y_bf16);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(B);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_kernel, yp, w, cnt, inv, d, k, y, y_bf16);
 }
 
 }  // namespace moe
