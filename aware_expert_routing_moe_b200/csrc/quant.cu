@@ -38,73 +38,116 @@ __device__ __forceinline__ unsigned pack4(float a, float b, float c, float d, fl
     return static_cast<unsigned>(lo) | (static_cast<unsigned>(hi) << 16);
 }
 
+// A lane's 16 columns: raw loads, the largest magnitude, and the four words
+// of e4m3 values.
 template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
+struct Lane16;
 template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) {
-    return __ldg(reinterpret_cast<const float4 *>(p));
-}
+struct Lane16<float> {
+    float4 v[4];
+    __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const float4 *>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ unsigned top() const {
+        unsigned t = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t = max(max(t, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu)),
+                    max(__float_as_uint(v[i].z) & 0x7fffffffu, __float_as_uint(v[i].w) & 0x7fffffffu));
+        return t;
+    }
+    __device__ __forceinline__ uint4 pack(float inv) const {
+        return make_uint4(pack4(v[0].x, v[0].y, v[0].z, v[0].w, inv), pack4(v[1].x, v[1].y, v[1].z, v[1].w, inv),
+                          pack4(v[2].x, v[2].y, v[2].z, v[2].w, inv), pack4(v[3].x, v[3].y, v[3].z, v[3].w, inv));
+    }
+};
 template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xffff0000u));
-}
-__device__ __forceinline__ unsigned abs_bits(const float4 &v) {
-    const unsigned a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
-    const unsigned c = __float_as_uint(v.z) & 0x7fffffffu, d = __float_as_uint(v.w) & 0x7fffffffu;
-    return max(max(a, b), max(c, d));
-}
+struct Lane16<__nv_bfloat16> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        v[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        v[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+    static __device__ __forceinline__ unsigned top2(unsigned w) { return max((w << 16) & 0x7fffffffu, w & 0x7fff0000u); }
+    __device__ __forceinline__ unsigned top() const {
+        return max(max(max(top2(v[0].x), top2(v[0].y)), max(top2(v[0].z), top2(v[0].w))),
+                   max(max(top2(v[1].x), top2(v[1].y)), max(top2(v[1].z), top2(v[1].w))));
+    }
+    static __device__ __forceinline__ unsigned pack2(unsigned a, unsigned b, float inv) {
+        return pack4(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+                     __uint_as_float(b & 0xffff0000u), inv);
+    }
+    __device__ __forceinline__ uint4 pack(float inv) const {
+        return make_uint4(pack2(v[0].x, v[0].y, inv), pack2(v[0].z, v[0].w, inv), pack2(v[1].x, v[1].y, inv),
+                          pack2(v[1].z, v[1].w, inv));
+    }
+};
 
-// A warp per block of 128 columns: four columns a lane.  Scale of row r,
-// block j at scale[r * pitch + j].
+// A warp per 512 columns of a row: 16 columns a lane (16-byte loads and one
+// 16-byte store), eight lanes a block of 128.  Scale of row r, block j at
+// scale[r * pitch + j].
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, long long rows, int cols, int cb,
-                                                            const int32_t *__restrict__ src, int n_src,
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, unsigned rows, int cols,
+                                                            unsigned chunks, const int32_t *__restrict__ src, int n_src,
                                                             uint8_t *__restrict__ q, float *__restrict__ scale,
                                                             int pitch, int32_t *__restrict__ zero, int n_zero) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    const long long first = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const unsigned warps = gridDim.x * 8;
     if (zero != nullptr)
-        for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n_zero; i += warps * 32) zero[i] = 0;
-    for (long long b = first; b < rows * cb; b += warps) {
-        const long long r = b / cb;
-        const int j = static_cast<int>(b - r * cb), c = j * BLK + lane * 4;
+        for (int i = blockIdx.x * 256 + threadIdx.x; i < n_zero; i += gridDim.x * 256) zero[i] = 0;
+    const unsigned items = rows * chunks;
+    for (unsigned b = blockIdx.x * 8 + (threadIdx.x >> 5); b < items; b += warps) {
+        const unsigned r = b / chunks;
+        const int c = static_cast<int>(b - r * chunks) * 512 + lane * 16;
         long long from = r;
         if (src != nullptr) {
             from = __ldg(src + r);
             if (from < 0 || from >= n_src) continue;  // past the last entry (or a bad list, reported by the product)
         }
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < cols) v = load4<T>(x + from * cols + c);
-        const int e = scale_exp(__reduce_max_sync(ALL, abs_bits(v)));
-        if (c < cols) *reinterpret_cast<unsigned *>(q + r * cols + c) = pack4(v.x, v.y, v.z, v.w, pow2(-e));
-        if (lane == 0) scale[r * pitch + j] = pow2(e);
+        Lane16<T> v;
+        if (c < cols) v.load(x + from * cols + c);
+        else v.zero();
+        unsigned top = v.top();
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(ALL, top, o));
+        const int e = scale_exp(top);
+        if (c < cols) {
+            *reinterpret_cast<uint4 *>(q + static_cast<long long>(r) * cols + c) = v.pack(pow2(-e));
+            if ((lane & 7) == 0) scale[static_cast<long long>(r) * pitch + c / BLK] = pow2(e);
+        }
+        if (b + warps < b) break;  // the counter would wrap
     }
 }
 
-// A block of 256 threads per 128 x 128 tile: warp w takes rows w, w + 8, ...
+// A block of 256 threads per 128 x 128 tile: eight lanes a row, 32 rows at a
+// time, all of the tile's loads in flight at once.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ x, int rows, int cols, int rb,
                                                              int cb, uint8_t *__restrict__ q,
                                                              float *__restrict__ scale) {
     __shared__ unsigned s_top[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long tile = blockIdx.x;
-    const int bc = static_cast<int>(tile % cb), br = static_cast<int>(tile / cb % rb);
-    const long long base = tile / (static_cast<long long>(cb) * rb) * rows * cols;
-    const int c = bc * BLK + lane * 4;
-    float4 v[16];
+    const unsigned tile = blockIdx.x, line = tile / cb;
+    const int bc = static_cast<int>(tile - line * cb), br = static_cast<int>(line % rb);
+    const long long base = static_cast<long long>(line / rb) * rows * cols;
+    const int c = bc * BLK + (lane & 7) * 16, r0 = br * BLK + warp * 4 + (lane >> 3);
+    Lane16<T> v[4];
     unsigned top = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = br * BLK + warp + 8 * i;
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows && c < cols) v[i] = load4<T>(x + base + static_cast<long long>(r) * cols + c);
-        top = max(top, abs_bits(v[i]));
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
+        if (r < rows && c < cols) v[i].load(x + base + static_cast<long long>(r) * cols + c);
+        else v[i].zero();
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, v[i].top());
     top = __reduce_max_sync(ALL, top);
     if (lane == 0) s_top[warp] = top;
     __syncthreads();
@@ -113,11 +156,10 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
     const int e = scale_exp(top);
     const float inv = pow2(-e);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = br * BLK + warp + 8 * i;
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 32 * i;
         if (r < rows && c < cols)
-            *reinterpret_cast<unsigned *>(q + base + static_cast<long long>(r) * cols + c) =
-                pack4(v[i].x, v[i].y, v[i].z, v[i].w, inv);
+            *reinterpret_cast<uint4 *>(q + base + static_cast<long long>(r) * cols + c) = v[i].pack(inv);
     }
     if (threadIdx.x == 0) scale[tile] = pow2(e);
 }
@@ -167,14 +209,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 namespace {
 cudaError_t launch_rows(const void *x, int type, long long rows, int cols, const int32_t *src, int n_src, uint8_t *q,
                         float *scale, int pitch, int32_t *zero, int n_zero, cudaStream_t s) {
-    const int cb = blocks_of(cols);
-    const long long blocks = rows * cb;
-    const unsigned grid = static_cast<unsigned>(blocks + 7 < 8 * 148 * 16 ? (blocks + 7) / 8 : 148 * 16);
+    const unsigned chunks = (cols + 511) / 512, n = static_cast<unsigned>(rows);
+    const long long blocks = (rows * chunks + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
     if (type == MOE_BF16)
-        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, cb, src, n_src, q,
+        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), n, cols, chunks, src, n_src, q,
                                                   scale, pitch, zero, n_zero);
     else
-        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), rows, cols, cb, src, n_src, q, scale,
+        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), n, cols, chunks, src, n_src, q, scale,
                                                   pitch, zero, n_zero);
     return cudaGetLastError();
 }
