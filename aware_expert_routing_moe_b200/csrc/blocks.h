@@ -21,7 +21,8 @@ inline int scale_pitch(int cols) { return (blocks_of(cols) + 3) / 4 * 4; }
 struct BlocksControl {
     int32_t error;
     int32_t next_tile, exits;  // product kernel: tiles claimed, CTAs finished (zero between calls)
-    int32_t pad[61];
+    uint32_t ticket;           // router: blocks finished (zero between calls)
+    int32_t pad[60];
 };
 static_assert(sizeof(BlocksControl) <= MOE_GEMM_WORKSPACE_BYTES, "control segment does not fit");
 

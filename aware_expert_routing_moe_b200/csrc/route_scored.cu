@@ -6,57 +6,59 @@
 //                       per run of tokens; an entry's place is the expert's
 //                       first place + the entries of earlier runs + its rank
 //                       among the run's tokens (bit masks, no atomics on
-//                       places: the lists do not depend on scheduling).  A
-//                       batch that is one run gets its lists in the first
-//                       kernel.
+//                       places: the lists do not depend on scheduling).
+// Batches of up to ONE_LAUNCH tokens get their lists from the last block of
+// the first kernel to finish.
 //
-// The choice is that of the values c = s + bias in fp64 (equal values to the
-// lower index).  The warp ranks fp32 values instead and checks that every
-// two neighbours of the order it uses, the first expert left out among them,
-// are further apart than the fp32 errors; a token that fails the check (a
-// few in 10^5 of random ones, and every exact tie) is done again in fp64.
-// Without a bias, and with groups valued by their best expert, the logits
-// themselves rank (a score is monotone in its logit).
+// The choice is that of the values c = s + bias in fp64, equal values to the
+// lower index.  The scores are computed in fp64 by a short exp and a
+// reciprocal (about 25 operations an expert); the warp then ranks 28-bit
+// images of the values, which one warp reduction each finds the largest of,
+// and ranks the fp64 values themselves only for a token in which two
+// neighbours of the order it uses are too close for that (about one in 10^4
+// random tokens, and every exact tie).  Without a bias, and with groups
+// valued by their best expert, the logits rank (a score is monotone in its
+// logit) and no score but the chosen ones is computed.
 #include <cfloat>
 #include <cmath>
 
 #include "blocks.h"
-#include "route_dev.cuh"
 
 namespace moe {
 namespace {
 
-constexpr unsigned ALL = FULL;
-constexpr int SUB = 64;          // tokens whose choices of one expert are one 64-bit mask
-constexpr int RUNS_MAX = 128;    // runs of tokens (blocks)
-constexpr int ONE_RUN = 128;     // 4 tokens a warp, but one launch
-constexpr int CHOOSE_THREADS = 1024;
-constexpr int LISTS_THREADS = 1024;
+constexpr unsigned ALL = 0xffffffffu;
+constexpr int SUB = 32;          // tokens whose choices of one expert are one 32-bit mask
+constexpr int RUNS_MAX = 256;    // runs of tokens (blocks) of a long batch
+constexpr int THREADS = 512;     // of both kernels
+constexpr int WARPS = THREADS / 32;
+// One launch up to this many tokens, a token per warp; the last block's work
+// grows with the batch, and above it the second kernel is cheaper.
+constexpr int ONE_LAUNCH = 512;
 
-// Tokens per run: a multiple of SUB that leaves at most RUNS_MAX runs; up to
-// ONE_RUN tokens are one.
+// Tokens per block of the first kernel.
 int run_tokens(int B) {
-    if (B <= ONE_RUN) return ONE_RUN;
+    if (B <= ONE_LAUNCH) return WARPS;
     const int subs = (B + SUB - 1) / SUB;
     return SUB * ((subs + RUNS_MAX - 1) / RUNS_MAX);
 }
 
-// Values of a token's row in shared memory: skewed by one every 32, so that
-// lanes which walk runs of experts meet different banks.
-__host__ __device__ constexpr int row_values(int E) { return E + E / 32 + 1; }
+// Counts of a run: whole 16-byte pieces.
+__host__ __device__ constexpr int hist_pitch(int E) { return (E + 7) / 8 * 8; }
 
 struct RouteArgs {
     const float *logits, *bias;
-    int B, E, k, run, runs;
+    int B, E, k, run, runs, one_launch;
     moe_scoring_t rule;
     int32_t *sel_idx;
     float *sel_w;
-    int32_t *hist;  // [runs][E]
+    unsigned *ticket;  // blocks finished (one launch)
+    uint16_t *hist;    // [runs][hist_pitch(E)]
     moe_lists_t lists;
 };
 
-// Largest value over the warp; the lowest expert index among equal ones
-// (value -inf: no candidate).
+// Largest value over the warp; the lowest index among equal ones (value
+// -inf: no candidate).
 __device__ __forceinline__ void warp_best(double &v, int &e) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -73,277 +75,282 @@ __device__ __forceinline__ double warp_sum(double v) {
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
     return v;
 }
-
-// A token in fp64.
-template <int NI>
-__device__ __noinline__ void token_exact(const RouteArgs &a, int b, unsigned *s_hist, double *s_row) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.rule.groups, per = a.E / G;
-            double s[NI], c[NI];
-            float l[NI];
-            double top = -INFINITY;
-    #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
-                float v = e < a.E ? __ldg(a.logits + static_cast<size_t>(b) * a.E + e) : -INFINITY;
-                v = v != v ? -INFINITY : fminf(v, FLT_MAX);
-                l[i] = v;
-                top = fmax(top, static_cast<double>(v));
-            }
-            if (a.rule.score == MOE_SCORE_SOFTMAX) {
-                int dummy = 0;
-                warp_best(top, dummy);
-                double sum = 0.0;
-    #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    s[i] = l[i] > -INFINITY ? exp(static_cast<double>(l[i]) - top) : 0.0;
-                    sum += s[i];
-                }
-                sum = warp_sum(sum);
-    #pragma unroll
-                for (int i = 0; i < NI; ++i) s[i] = s[i] / sum;
-            } else {
-    #pragma unroll
-                for (int i = 0; i < NI; ++i) s[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
-            }
-    #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
-                const double beta = a.bias != nullptr && e < a.E ? static_cast<double>(__ldg(a.bias + e)) : 0.0;
-                c[i] = l[i] > -INFINITY ? s[i] + beta : -INFINITY;
-            }
-            if (G > 1) {
-                // lane g sums the best of group g (rows skewed by one value every 32)
-                double *row = s_row + static_cast<size_t>(warp) * row_values(a.E);
-                __syncwarp();
-    #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.E) row[e + (e >> 5)] = c[i];
-                }
-                __syncwarp();
-                double b1 = -INFINITY, b2 = -INFINITY;
-                if (lane < G) {
-                    for (int j = 0; j < per; ++j) {
-                        const int e = lane * per + j;
-                        const double v = row[e + (e >> 5)];
-                        if (v > b1) {
-                            b2 = b1;
-                            b1 = v;
-                        } else if (v > b2) b2 = v;
-                    }
-                }
-                double value = b1;
-                if (a.rule.group_best == 2 && b2 > -INFINITY) value += b2;
-                unsigned keep = 0;
-                for (int j = 0; j < a.rule.top_groups; ++j) {
-                    double v = (keep >> lane) & 1u ? -INFINITY : value;
-                    int g = lane;
-                    warp_best(v, g);
-                    if (v > -INFINITY) keep |= 1u << g;
-                }
-    #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < a.E && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
-                }
-            }
-            int mine = -1;        // lane j: the j-th chosen expert and its score
-            double score = 0.0;
-            for (int j = 0; j < a.k; ++j) {
-                double v = -INFINITY, sv = 0.0;
-                int e = 1 << 20;
-    #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    if (c[i] > v) {
-                        v = c[i];
-                        e = lane + 32 * i;
-                        sv = s[i];
-                    }
-                const int own = e;
-                warp_best(v, e);
-                if (v == -INFINITY) break;
-                sv = __shfl_sync(ALL, sv, e & 31);
-                if (own == e) {
-    #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (lane + 32 * i == e) c[i] = -INFINITY;
-                    atomicAdd(s_hist + e, 1u);
-                }
-                if (lane == j) {
-                    mine = e;
-                    score = sv;
-                }
-            }
-            const double sum = a.rule.renorm ? warp_sum(score) : 1.0;
-            if (lane < a.k) {
-                a.sel_idx[static_cast<size_t>(b) * a.k + lane] = mine;
-                a.sel_w[static_cast<size_t>(b) * a.k + lane] =
-                    mine >= 0 && sum > 0.0 ? static_cast<float>(score / sum * static_cast<double>(a.rule.scale)) : 0.0f;
-            }
+__device__ __forceinline__ float warp_maxf(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
+    return v;
 }
 
-// fp32 errors, in units of 2^-24: exp_own (1 ulp = 2 units), the sum 1 + z,
-// and a division good to 2 ulp give a sigmoid within 8 units of itself; a
-// softmax adds the errors of the sum's terms (2) and of the sum, taken in
-// fp64, and stays within 8.  Adding the bias rounds once more.
-constexpr float ERR = 5.9604645e-8f * 9.0f;
-// Logits: scores differ in fp64 when their logits do, by more than
-// NEAR_LOGIT and inside these limits.
-constexpr float NEAR_LOGIT = 1e-9f, TOP_LOGIT = 16.0f, LOW_LOGIT = -600.0f;
+// Adding this to |v| < 2^31 rounds v to an integer, found in the low word.
+constexpr double ROUND = 6755399441055744.0;  // 1.5 * 2^52
 
-// The lane's best candidate.
+// exp(x) for x <= 0 in fp64: x = n ln2 + r with ln2 split into its first 32
+// bits and a tail, the Taylor series of exp(r) to degree 12 (|r| <= 0.347:
+// the rest is below 2e-16), 2^n through the exponent field.  -700 <= x.
+__device__ __forceinline__ double exp_neg(double x) {
+    const double t = fma(x, 1.4426950408889634, ROUND), n = t - ROUND;
+    double r = fma(n, -2977044472.0 / 4294967296.0, x);
+    r = fma(n, 4.2009150726810846e-11, r);
+    double p = 1.0 / 479001600.0;
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+}
+// 1 / y for 1 <= y <= 2: an fp32 reciprocal and two Newton steps.
+__device__ __forceinline__ double reciprocal(double y) {
+    double r = static_cast<double>(__fdividef(1.0f, static_cast<float>(y)));
+    r = fma(r, fma(-y, r, 1.0), r);
+    return fma(r, fma(-y, r, 1.0), r);
+}
+__device__ __forceinline__ double sigmoid(float l) {
+    const double z = exp_neg(static_cast<double>(fmaxf(-fabsf(l), -700.0f)));
+    const double r = reciprocal(1.0 + z);
+    return l >= 0.0f ? r : z * r;
+}
+// exp(l - top); exp(-700) below
+__device__ __forceinline__ double exp_from(float l, float top) {
+    return exp_neg(fmax(static_cast<double>(l) - static_cast<double>(top), -700.0));
+}
+__device__ __forceinline__ int round_int(double v) { return __double2loint(v + ROUND); }
+
+// Logits for which fp64 scores keep the order of the logits.
+constexpr float TOP_LOGIT = 16.0f, LOW_LOGIT = -600.0f;
+// Images: 27 bits of value (a unit is 2^-26 of the largest magnitude, at
+// most) over 4 bits of slot.  Rounding moves a value by half a unit, so two
+// that are more than NEAR units apart are in order; sums of two, SUM_NEAR.
+constexpr int SLOT_BITS = 4, NEAR = 2, SUM_NEAR = 4;
+
+// Experts lane + 32 i, i < NI.
 template <int NI>
-__device__ __forceinline__ void lane_best(const float (&c)[NI], int lane, float &v, int &e) {
-    v = -INFINITY;
-    e = 1 << 20;
+struct Token {
+    double c[NI];       // values; -inf: not to choose from
+    unsigned image[NI]; // 0: not to choose from
+
+    // Groups whose experts stay, and the choice (lane j: the j-th expert,
+    // -1 none), by the images; false: too close to call.
+    __device__ __forceinline__ bool by_image(const RouteArgs &a, const int (&group)[NI], unsigned *row, int &mine) {
+        const int lane = threadIdx.x & 31;
+        bool sure = true;
+        if (a.rule.groups > 1) {
+            const int G = a.rule.groups, per = a.E / G;
+            __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-        if (c[i] > v) {
-            v = c[i];
-            e = lane + 32 * i;
+            for (int i = 0; i < NI; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.E) row[e + group[i]] = image[i] >> SLOT_BITS;  // groups skewed by a bank each
+            }
+            __syncwarp();
+            unsigned b1 = 0u, b2 = 0u;
+            if (lane < G) {
+                const unsigned *mem = row + lane * (per + 1);
+#pragma unroll 8
+                for (int j = 0; j < per; ++j) {
+                    const unsigned v = mem[j];
+                    b2 = max(b2, min(b1, v));
+                    b1 = max(b1, v);
+                }
+            }
+            // a group of one such expert has half the sum: too close to say
+            const bool two = a.rule.group_best == 2;
+            if (two && __any_sync(ALL, b1 != 0u && b2 == 0u)) return false;
+            unsigned value = two ? b1 + b2 : b1, keep = 0u, before = 0xffffffffu;
+            const unsigned near = two ? SUM_NEAR : NEAR;
+            for (int j = 0; j <= a.rule.top_groups; ++j) {
+                const unsigned m = __reduce_max_sync(ALL, value);
+                if (m == 0u) break;
+                sure = sure && before - m > near;
+                before = m;
+                if (j == a.rule.top_groups) break;
+                const int g = __ffs(__ballot_sync(ALL, value == m)) - 1;
+                keep |= 1u << g;
+                if (lane == g) value = 0u;
+            }
+            if (!sure) return false;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (!((keep >> group[i]) & 1u)) image[i] = 0u;
         }
-}
-
-// Experts lane + 32 i, i < NI; false: the token has to be decided in fp64
-// (nothing has been written).
-template <int NI>
-__device__ __forceinline__ bool token_fast(const RouteArgs &a, int b, unsigned *s_hist, float *row) {
-    const int lane = threadIdx.x & 31;
-    const int G = a.rule.groups;
-    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID;
-    const bool by_logit = a.bias == nullptr && (G == 1 || a.rule.group_best == 1);
-    float l[NI], s[NI], c[NI];
-    float top = -INFINITY, low = INFINITY;
+        unsigned best = 0u, before = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        const float v = e < a.E ? __ldg(a.logits + static_cast<size_t>(b) * a.E + e) : -INFINITY;
-        l[i] = v != v ? -INFINITY : fminf(v, FLT_MAX);
-        top = fmaxf(top, l[i]);
+        for (int i = 0; i < NI; ++i) best = max(best, image[i]);
+        mine = -1;
+        for (int j = 0; j <= a.k; ++j) {
+            const unsigned m = __reduce_max_sync(ALL, best);
+            if (m == 0u) break;
+            const unsigned who = __ballot_sync(ALL, best == m);
+            sure = sure && (before >> SLOT_BITS) - (m >> SLOT_BITS) > NEAR && (who & (who - 1u)) == 0u;
+            before = m;
+            if (j == a.k) break;
+            if (lane == j) mine = (__ffs(who) - 1) + 32 * static_cast<int>((1u << SLOT_BITS) - 1u - (m & ((1u << SLOT_BITS) - 1u)));
+            best = 0u;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {  // (another lane's equal image makes the token unsure)
+                if (image[i] == m) image[i] = 0u;
+                best = max(best, image[i]);
+            }
+        }
+        return sure;
     }
-    top = float_of_ord(__reduce_max_sync(ALL, ord_of(top)));
-    float shift = 0.0f, bound = 1.0f;  // bound: no score is larger
-    double z = 1.0;
-    if (sigmoid) {
+};
+
+    // The same by the values c (overwritten).
+    template <int NI>
+__device__ __noinline__ int by_value(const RouteArgs &a, double (&c)[NI], double *row) {
+        const int lane = threadIdx.x & 31;
+        const int G = a.rule.groups, per = a.E / G;
+        if (G > 1) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
+            __syncwarp();
+            double b1 = -INFINITY, b2 = -INFINITY;
+            if (lane < G)
+                for (int j = 0; j < per; ++j) {
+                    const double v = row[lane * per + j];
+                    if (v > b1) {
+                        b2 = b1;
+                        b1 = v;
+                    } else if (v > b2) b2 = v;
+                }
+            double value = b1;
+            if (a.rule.group_best == 2 && b2 > -INFINITY) value += b2;
+            unsigned keep = 0;
+            for (int j = 0; j < a.rule.top_groups; ++j) {
+                double v = (keep >> lane) & 1u ? -INFINITY : value;
+                int g = lane;
+                warp_best(v, g);
+                if (v > -INFINITY) keep |= 1u << g;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.E && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
+            }
+        }
+        int mine = -1;
+        for (int j = 0; j < a.k; ++j) {
+            double v = -INFINITY;
+            int e = 1 << 20;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (c[i] > v) {
+                    v = c[i];
+                    e = lane + 32 * i;
+                }
+            warp_best(v, e);
+            if (v == -INFINITY) break;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (lane + 32 * i == e) c[i] = -INFINITY;
+            if (lane == j) mine = e;
+        }
+        return mine;
+    }
+
+__device__ __forceinline__ float clean_logit(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
+
+// A token's choice and weights by one warp.
+template <int NI>
+__device__ __forceinline__ void choose(const RouteArgs &a, int b, const int (&group)[NI], const float (&bias)[NI],
+                                       double unit, unsigned *s_hist, double *row, int *s_sel, float *s_w) {
+    const int lane = threadIdx.x & 31;
+    const bool sig = a.rule.score == MOE_SCORE_SIGMOID;
+    const float *logits = a.logits + static_cast<size_t>(b) * a.E;
+    Token<NI> t;
+    float l[NI], top = -INFINITY, low = INFINITY;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) l[i] = lane + 32 * i < a.E ? clean_logit(__ldg(logits + lane + 32 * i)) : -INFINITY;
+    // with a bias, or groups valued by two experts, the values rank
+    const bool may_logit = a.bias == nullptr && (a.rule.groups == 1 || a.rule.group_best == 1);
+    if (may_logit || !sig) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const float x = exp_own(-fabsf(l[i]));  // 0 for -inf
-            s[i] = __fdividef(l[i] >= 0.0f ? 1.0f : x, 1.0f + x);
+            top = fmaxf(top, l[i]);
+            if (l[i] > -INFINITY) low = fminf(low, l[i]);
         }
-        if (top > TOP_LOGIT && by_logit) return false;
-    } else {
-        shift = top > -INFINITY ? top : 0.0f;
+        top = warp_maxf(top);
+        low = -warp_maxf(-low);
+    }
+    const float shift = sig || top == -INFINITY ? 0.0f : top;
+    const bool by_logit = may_logit && (!sig || top <= TOP_LOGIT) && low - shift >= LOW_LOGIT;
+    // softmax: the sum of exp(l - top)
+    double z = 1.0;
+    if (!sig && !(by_logit && a.rule.renorm)) {
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            s[i] = exp_own(l[i] - shift);
-            sum += static_cast<double>(s[i]);
+            t.c[i] = l[i] > -INFINITY ? exp_from(l[i], shift) : 0.0;
+            sum += t.c[i];
         }
         z = warp_sum(sum);
-        const float inv = z > 0.0 ? static_cast<float>(1.0 / z) : 0.0f;
-        bound = inv;
-        if (!by_logit) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) s[i] *= inv;
-        }
     }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        if (by_logit) c[i] = l[i];
-        else {
-            const float beta = a.bias != nullptr && e < a.E ? __ldg(a.bias + e) : 0.0f;
-            c[i] = l[i] > -INFINITY ? s[i] + beta : -INFINITY;
-            bound = fmaxf(bound, c[i] > -INFINITY ? fabsf(c[i]) : 0.0f);
-        }
-    }
-    // two values further apart than this are in order
-    float near = NEAR_LOGIT;
-    if (!by_logit) near = 2.0f * ERR * __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bound)));
-    bool sure = true;
-    if (G > 1) {
-        const int per = a.E / G;
-        __syncwarp();
+    constexpr unsigned LAST_SLOT = (1u << SLOT_BITS) - 1u;
+    if (by_logit) {
+        // images of the upper 64 units of logit; what lies below is equal
+        const double base = 64.0 - static_cast<double>(top);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) row[e + (e >> 5)] = c[i];
+            t.c[i] = static_cast<double>(l[i]);
+            const int u = round_int(fmax(t.c[i] + base, 0.0) * 1048576.0) + 1;
+            t.image[i] = l[i] > -INFINITY ? static_cast<unsigned>(u) << SLOT_BITS | (LAST_SLOT - i) : 0u;
         }
-        __syncwarp();
-        float b1 = -INFINITY, b2 = -INFINITY;
-        if (lane < G) {
-#pragma unroll 8
-            for (int j = 0; j < per; ++j) {
-                const int e = lane * per + j;
-                const float v = row[e + (e >> 5)];
-                b2 = fmaxf(b2, fminf(b1, v));
-                b1 = fmaxf(b1, v);
-            }
-        }
-        float value = b1;
-        if (a.rule.group_best == 2 && b2 > -INFINITY) value += b2;
-        // a sum of two values rounds once more: three times the distance
-        const float gnear = a.rule.group_best == 2 ? 3.0f * near : near;
-        unsigned keep = 0;
-        float before = INFINITY;
-        for (int j = 0; j <= a.rule.top_groups; ++j) {
-            const unsigned o = (keep >> lane) & 1u || lane >= G ? 0u : ord_of(value);
-            const unsigned m = __reduce_max_sync(ALL, o);
-            const float v = m == 0u ? -INFINITY : float_of_ord(m);
-            if (v == -INFINITY) break;
-            sure = sure && (before - v > gnear || (by_logit && before == v));
-            before = v;
-            if (j < a.rule.top_groups) keep |= 1u << (__ffs(__ballot_sync(ALL, o == m)) - 1);
-        }
+    } else {
+        const double inv = sig ? 1.0 : z > 0.0 ? 1.0 / z : 0.0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
+            const double s = sig ? sigmoid(l[i]) : t.c[i] * inv;
+            t.c[i] = l[i] > -INFINITY ? s + static_cast<double>(bias[i]) : -INFINITY;
+            const int u = round_int(l[i] > -INFINITY ? t.c[i] * unit : 0.0) + (1 << 26) + 1;
+            t.image[i] = l[i] > -INFINITY ? static_cast<unsigned>(u) << SLOT_BITS | (LAST_SLOT - i) : 0u;
         }
     }
-    int mine = -1;  // lane j: the j-th chosen expert and its score
-    float score = 0.0f, v, before = INFINITY;
-    int e;
-    lane_best<NI>(c, lane, v, e);
-    for (int j = 0; j <= a.k; ++j) {
-        const unsigned o = v == -INFINITY ? 0u : ord_of(v);
-        const unsigned m = __reduce_max_sync(ALL, o);
-        if (m == 0u) break;
-        const float best = float_of_ord(m);
-        sure = sure && (before - best > near || (by_logit && before == best));
-        before = best;
-        low = fminf(low, best);
-        if (j == a.k) break;
-        const int win = static_cast<int>(__reduce_min_sync(ALL, o == m ? static_cast<unsigned>(e) : 0xffffffffu));
-        float sv = 0.0f;
-        if (win == e) {
+    int mine;
+    if (!t.by_image(a, group, reinterpret_cast<unsigned *>(row), mine)) {
+        double c[NI];  // a copy: the values themselves stay in registers
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == e) {
-                    sv = s[i];
-                    c[i] = -INFINITY;
-                }
-            lane_best<NI>(c, lane, v, e);
-        }
-        sv = __shfl_sync(ALL, sv, win & 31);
-        if (lane == j) {
-            mine = win;
-            score = sv;
-        }
+        for (int i = 0; i < NI; ++i) c[i] = t.c[i];
+        mine = by_value<NI>(a, c, row);
     }
-    if (by_logit) sure = sure && low - shift > LOW_LOGIT;
-    // scores that fp32 cannot hold (exp_own gives 0 below -87) weigh in fp64
-    if (!sure || __any_sync(ALL, mine >= 0 && score < 1e-30f)) return false;
-    const double sum = a.rule.renorm ? warp_sum(static_cast<double>(score)) : (sigmoid || !by_logit ? 1.0 : z);
+    // lane j: the score of its expert
+    double s = 0.0;
+    if (mine >= 0) {
+        const float v = clean_logit(__ldg(logits + mine));
+        s = sig ? (v >= -700.0f ? sigmoid(v) : 0.0) : exp_from(v, shift);
+    }
+    const double sum = a.rule.renorm ? warp_sum(s) : z;
     if (lane < a.k) {
+        float w = 0.0f;
+        if (mine >= 0 && sum > 0.0)
+            w = sum > 1e-30 && s > 1e-30 ? static_cast<float>(s) / static_cast<float>(sum) * a.rule.scale
+                                         : static_cast<float>(s / sum * static_cast<double>(a.rule.scale));
         a.sel_idx[static_cast<size_t>(b) * a.k + lane] = mine;
-        a.sel_w[static_cast<size_t>(b) * a.k + lane] =
-            mine >= 0 ? static_cast<float>(static_cast<double>(score) * static_cast<double>(a.rule.scale) / sum) : 0.0f;
-        if (mine >= 0) atomicAdd(s_hist + mine, 1u);
+        a.sel_w[static_cast<size_t>(b) * a.k + lane] = w;
+        if (a.runs == 1) {
+            s_sel[b * a.k + lane] = mine;
+            s_w[b * a.k + lane] = w;
+        }
+        if (mine >= 0 && !a.one_launch) atomicAdd(s_hist + mine, 1u);
     }
-    return true;
 }
+
+// ---------------------------------------------------------------- lists --
+struct ListsShared {
+    int total[SE_MAX], before[SE_MAX], place[SE_MAX], wsum[WARPS];
+    unsigned mask[SE_MAX];
+    int sel[WARPS * K_MAX];  // the choices of a batch that is one block
+    float w[WARPS * K_MAX];
+};
 
 // Inclusive scan over the block's threads.
 __device__ int block_scan(int v, int *wsum) {
@@ -355,54 +362,77 @@ __device__ int block_scan(int v, int *wsum) {
     }
     if (lane == 31) wsum[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int w = wsum[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(ALL, w, o);
-            if (lane >= o) w += u;
-        }
-        wsum[lane] = w;
-    }
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += wsum[w];
     __syncthreads();
-    const int r = v + (warp > 0 ? wsum[warp - 1] : 0);
-    __syncthreads();
-    return r;
+    return v + base;
 }
 
-// The lists of the block's run (all the block's threads).
-__device__ void lists_of_run(const RouteArgs &a) {
-    __shared__ int s_total[SE_MAX], s_before[SE_MAX], s_place[SE_MAX], wsum[32];
-    __shared__ unsigned long long s_mask[SE_MAX];
-    const int tid = threadIdx.x;
-    for (int e = tid; e < SE_MAX; e += LISTS_THREADS) {
-        s_total[e] = s_before[e] = 0;
-        s_mask[e] = 0ull;
-    }
+// Masks of the SUB tokens from t0 (their choices), then fn(expert, token,
+// pair) for each choice.
+template <class Fn>
+__device__ __forceinline__ void each_choice(const RouteArgs &a, int t0, int last, ListsShared &sh, Fn fn) {
+    const int p = threadIdx.x, t = p / a.k;  // at most 512 pairs: one a thread
+    const size_t pair = static_cast<size_t>(t0) * a.k + p;
+    int e = -1;
+    if (p < min(SUB, last - t0) * a.k) e = a.runs == 1 ? sh.sel[p] : __ldcg(a.sel_idx + pair);
+    if (e >= 0) atomicOr(sh.mask + e, 1u << t);
     __syncthreads();
-    // the run counts, several runs at once
-    const int parts = LISTS_THREADS / a.E, part = tid / a.E, ex = tid - part * a.E;
-    if (part < parts) {
-        int total = 0, before = 0;
-        for (int r = part; r < a.runs; r += parts) {
-            const int h = a.hist[static_cast<size_t>(r) * a.E + ex];
-            total += h;
-            if (r < static_cast<int>(blockIdx.x)) before += h;
+    if (e >= 0) fn(e, t, pair);
+    __syncthreads();
+}
+
+// The lists' entries of tokens [first, last), and what one block (`head`)
+// writes for all.  Expert counts come from the runs' histograms, or, for one
+// launch, from the choices.
+__device__ void write_lists(const RouteArgs &a, ListsShared &sh, int first, int last, bool head) {
+    const int tid = threadIdx.x;  // SE_MAX threads: one an expert
+    sh.total[tid] = sh.before[tid] = 0;
+    sh.mask[tid] = 0u;
+    __syncthreads();
+    if (a.one_launch) {
+        for (int t0 = 0; t0 < a.B; t0 += SUB) {
+            each_choice(a, t0, a.B, sh, [](int, int, size_t) {});
+            sh.total[tid] += __popc(sh.mask[tid]);
+            sh.mask[tid] = 0u;
+            __syncthreads();
         }
-        if (total) atomicAdd(s_total + ex, total);
-        if (before) atomicAdd(s_before + ex, before);
+    } else {
+        // eight experts a thread, several runs at once
+        const int pieces = hist_pitch(a.E) / 8, parts = THREADS / pieces, part = tid / pieces, at = tid - part * pieces;
+        int total[8] = {}, before[8] = {};
+        if (part < parts) {
+            const uint4 *h = reinterpret_cast<const uint4 *>(a.hist) + at;
+#pragma unroll 8
+            for (int r = part; r < a.runs; r += parts) {
+                const uint4 v = __ldcg(h + r * pieces);
+                const unsigned w[4] = {v.x, v.y, v.z, v.w};
+                const bool earlier = r < static_cast<int>(blockIdx.x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int n = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
+                    total[i] += n;
+                    before[i] += earlier ? n : 0;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                atomicAdd(sh.total + at * 8 + i, total[i]);
+                atomicAdd(sh.before + at * 8 + i, before[i]);
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int n = tid < a.E ? s_total[tid] : 0;
-    const int end = block_scan(n, wsum), slot = block_scan(n > 0 ? 1 : 0, wsum);
+    const int n = tid < a.E ? sh.total[tid] : 0;
+    const int end = block_scan(n, sh.wsum), slot = block_scan(n > 0 ? 1 : 0, sh.wsum);
     __shared__ int s_end, s_slots;
-    if (tid == LISTS_THREADS - 1) {
+    if (tid == THREADS - 1) {
         s_end = end;
         s_slots = slot;
     }
-    if (tid < a.E) s_place[tid] = end - n + s_before[tid];
+    sh.place[tid] = end - n + sh.before[tid];
     __syncthreads();
-    if (blockIdx.x == 0 && tid < a.E) {
+    if (head && tid < a.E) {
         if (n > 0) {
             a.lists.active[slot - 1] = tid;
             a.lists.offsets[slot - 1] = end - n;
@@ -414,78 +444,97 @@ __device__ void lists_of_run(const RouteArgs &a) {
             *a.lists.n_active = s_slots;
         }
     }
-    const int first = blockIdx.x * a.run, last = min(first + a.run, a.B);
-    const long long all = static_cast<long long>(a.B) * a.k;
-    for (long long p = s_end + static_cast<long long>(blockIdx.x) * LISTS_THREADS + tid; p < all;
-         p += static_cast<long long>(gridDim.x) * LISTS_THREADS) {
+    const int all = a.B * a.k, blocks = a.one_launch ? 1 : gridDim.x, me = a.one_launch ? 0 : blockIdx.x;
+    for (int p = s_end + me * THREADS + tid; p < all; p += blocks * THREADS) {
         a.lists.tok[p] = -1;
         a.lists.w[p] = 0.0f;
     }
     for (int t0 = first; t0 < last; t0 += SUB) {
-        const int pairs = min(SUB, last - t0) * a.k;  // at most 1024
-        int e = -1, t = 0;
-        if (tid < pairs) {
-            t = tid / a.k;
-            e = a.sel_idx[static_cast<size_t>(t0) * a.k + tid];
-            if (e >= 0) atomicOr(s_mask + e, 1ull << t);
-        }
-        __syncthreads();
-        if (e >= 0) {
-            const int p = s_place[e] + __popcll(s_mask[e] & ((1ull << t) - 1ull));
+        each_choice(a, t0, last, sh, [&](int e, int t, size_t pair) {
+            const int p = sh.place[e] + __popc(sh.mask[e] & ((1u << t) - 1u));
             a.lists.tok[p] = t0 + t;
-            a.lists.w[p] = a.sel_w[static_cast<size_t>(t0) * a.k + tid];
-        }
-        __syncthreads();
-        if (tid < a.E) {
-            s_place[tid] += __popcll(s_mask[tid]);
-            s_mask[tid] = 0ull;
-        }
+            a.lists.w[p] = a.runs == 1 ? sh.w[pair] : __ldcg(a.sel_w + pair);
+        });
+        sh.place[tid] += __popc(sh.mask[tid]);
+        sh.mask[tid] = 0u;
         __syncthreads();
     }
 }
+static_assert(THREADS == SE_MAX && SUB * K_MAX <= THREADS, "a thread per expert, and per choice of SUB tokens");
 
 template <int NI>
-__global__ void __launch_bounds__(CHOOSE_THREADS, 1) route_choose_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(THREADS, NI <= 8 ? 2 : 1) route_choose_kernel(const __grid_constant__ RouteArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ unsigned char smem[];
-    unsigned *s_hist = reinterpret_cast<unsigned *>(smem);          // [E]
-    double *s_row = reinterpret_cast<double *>(smem + SE_MAX * 4);  // [warp][row_values(E)], groups only
-    const int warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < a.E; e += CHOOSE_THREADS) s_hist[e] = 0;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ ListsShared sh;
+    __shared__ int s_last;
+    unsigned *s_hist = reinterpret_cast<unsigned *>(sh.total);
+    double *s_row = reinterpret_cast<double *>(smem);  // [warp][E + groups], groups only
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    s_hist[threadIdx.x] = 0;
+    const int per = a.E / a.rule.groups;
+    int group[NI];
+    float bias[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = lane + 32 * i;
+        group[i] = a.rule.groups > 1 ? min(e, a.E - 1) / per : 0;
+        bias[i] = a.bias != nullptr && e < a.E ? __ldg(a.bias + e) : 0.0f;
+    }
+    // images: scores are at most 1, so values are below 1 + the largest bias
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) most = fmaxf(most, fabsf(bias[i]));
+    most = 1.0f + warp_maxf(most);
+    const int ex = static_cast<int>(__float_as_uint(most) >> 23) - 126;  // most < 2^ex
+    const double unit = __hiloint2double((1023 + 26 - ex) << 20, 0);
     __syncthreads();
     const int first = blockIdx.x * a.run, last = min(first + a.run, a.B);
-    for (int b = first + warp; b < last; b += CHOOSE_THREADS / 32)
-        if (!token_fast<NI>(a, b, s_hist, reinterpret_cast<float *>(s_row + static_cast<size_t>(warp) * row_values(a.E))))
-            token_exact<NI>(a, b, s_hist, s_row);
+    for (int b = first + warp; b < last; b += WARPS)
+        choose<NI>(a, b, group, bias, unit, s_hist, s_row + static_cast<size_t>(warp) * (a.E + a.rule.groups), sh.sel, sh.w);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += CHOOSE_THREADS) a.hist[static_cast<size_t>(blockIdx.x) * a.E + e] = s_hist[e];
-    if (a.runs == 1) {
-        __threadfence_block();
-        __syncthreads();
-        lists_of_run(a);
+    if (!a.one_launch) {
+        const int pitch = hist_pitch(a.E);
+        if (threadIdx.x < pitch)
+            a.hist[static_cast<size_t>(blockIdx.x) * pitch + threadIdx.x] = static_cast<uint16_t>(s_hist[threadIdx.x]);
+        return;
     }
+    if (a.runs == 1) {
+        write_lists(a, sh, 0, a.B, true);
+        return;
+    }
+    // the last block to finish writes the lists (the ticket wraps to 0)
+    if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atomicInc(a.ticket, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (s_last) write_lists(a, sh, 0, a.B, true);
 }
 
-__global__ void __launch_bounds__(LISTS_THREADS, 1) route_lists_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(THREADS) route_lists_kernel(const __grid_constant__ RouteArgs a) {
+    __shared__ ListsShared sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    lists_of_run(a);
+    const int first = blockIdx.x * a.run;
+    write_lists(a, sh, first, min(first + a.run, a.B), blockIdx.x == 0);
 }
 
 template <int NI>
 cudaError_t launch_choose(const RouteArgs &a, cudaStream_t s) {
-    const size_t rows = a.rule.groups > 1 ? static_cast<size_t>(CHOOSE_THREADS / 32) * row_values(a.E) * 8 : 0;
-    const size_t smem = SE_MAX * 4 + rows;
+    const size_t smem = a.rule.groups > 1 ? static_cast<size_t>(WARPS) * (a.E + a.rule.groups) * 8 : 0;
     static bool configured[MAX_DEVICES] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        err = cudaFuncSetAttribute(route_choose_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        err = cudaFuncSetAttribute(route_choose_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   WARPS * (SE_MAX + 32) * 8);
         if (err != cudaSuccess) return err;
         configured[dev] = true;
     }
-    route_choose_kernel<NI><<<a.runs, CHOOSE_THREADS, smem, s>>>(a);
+    route_choose_kernel<NI><<<a.runs, THREADS, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -493,13 +542,14 @@ cudaError_t launch_choose(const RouteArgs &a, cudaStream_t s) {
 
 size_t route_ws_bytes(const moe_dims_t &d) {
     const size_t run = run_tokens(d.B), runs = (d.B + run - 1) / run;
-    return (sizeof(BlocksControl) + runs * d.E * 4 + 255) / 256 * 256;
+    return (sizeof(BlocksControl) + (d.B <= ONE_LAUNCH ? 0 : runs * hist_pitch(d.E) * 2) + 255) / 256 * 256;
 }
 
 cudaError_t launch_route_scored(const float *logits, const float *bias, const moe_dims_t &d,
                                 const moe_scoring_t &r, int32_t *sel_idx, float *sel_w, const moe_lists_t &l,
                                 void *ws, cudaStream_t s) {
     RouteArgs a = {};
+    BlocksControl *control = static_cast<BlocksControl *>(ws);
     a.logits = logits;
     a.bias = bias;
     a.B = d.B;
@@ -507,21 +557,22 @@ cudaError_t launch_route_scored(const float *logits, const float *bias, const mo
     a.k = d.k;
     a.run = run_tokens(d.B);
     a.runs = (d.B + a.run - 1) / a.run;
+    a.one_launch = d.B <= ONE_LAUNCH;
     a.rule = r;
     a.sel_idx = sel_idx;
     a.sel_w = sel_w;
-    a.hist = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + sizeof(BlocksControl));
+    a.ticket = &control->ticket;
+    a.hist = reinterpret_cast<uint16_t *>(control + 1);
     a.lists = l;
     cudaError_t err = a.E <= 32    ? launch_choose<1>(a, s)
                       : a.E <= 64  ? launch_choose<2>(a, s)
                       : a.E <= 128 ? launch_choose<4>(a, s)
                       : a.E <= 256 ? launch_choose<8>(a, s)
                                    : launch_choose<16>(a, s);
-    if (err != cudaSuccess) return err;
-    if (a.runs == 1) return cudaSuccess;
+    if (err != cudaSuccess || a.one_launch) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.runs);
-    cfg.blockDim = dim3(LISTS_THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -348,10 +348,9 @@ size_t moe_route_workspace_bytes(moe_dims_t dims);
  * counts as the largest finite value; a token with fewer than k experts to
  * choose from gets -1 and weight 0 in the slots left (a token with none is
  * in no list: padding).  bias must be finite.  The choice follows the exact
- * values of c as far as fp64 tells them apart (a comparison that fp32
- * cannot decide is decided in fp64), so it does not depend on rounding.
- * Deterministic.  ws: moe_route_workspace_bytes(dims) bytes (no zeroing
- * needed). */
+ * values of c as far as fp64 tells them apart, not their fp32 roundings.
+ * Deterministic.  ws: moe_route_workspace_bytes(dims) bytes, 256-byte
+ * aligned, zero-filled once before its first use. */
 moe_status_t moe_route_scored(const float *logits, const float *bias, moe_dims_t dims, moe_scoring_t rule,
                               int32_t *sel_idx, float *sel_w, moe_lists_t lists, void *ws, size_t ws_bytes,
                               void *stream);
