@@ -16,6 +16,7 @@ general router ``moe_route_scored``; the block-scaled 8-bit operators
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -323,6 +324,30 @@ def moe_expert_ffn_channels(x, Wgate, Wup, WdownT, sel_idx, sel_w, score, c: int
     return y
 
 
+# The calls below are short on the GPU, so the binding keeps its own part
+# short: structures of the same numbers are built once, and the current
+# stream is read as a raw handle.
+@functools.lru_cache(maxsize=1024)
+def _dims(B: int, d: int, E: int, k: int, d_ff: int) -> Dims:
+    return Dims(B, d, E, k, d_ff)
+
+
+@functools.lru_cache(maxsize=256)
+def _scoring(score: int, groups: int, top_groups: int, group_best: int, renorm: int, scale: float) -> Scoring:
+    return Scoring(score, groups, top_groups, group_best, renorm, scale)
+
+
+def _stream_of(stream, t):
+    """Raw handle of the stream a call on tensor t runs on: t must be on the
+    current device."""
+    if stream is not None:
+        return _stream(stream)
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _dtype(t) -> int:
     code = _DTYPES.get(t if isinstance(t, torch.dtype) else t.dtype)
     if code is None:
@@ -372,9 +397,10 @@ def moe_route_scored(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, 
     if ws is None:
         ws = new_route_workspace(B, E, k, logits.device)
     sel, w = out
-    st = load_library().moe_route_scored(_ptr(logits), _ptr(bias), Dims(B, 0, E, k, 0),
-                                         Scoring(score, groups, top_groups, group_best, int(renorm), scale),
-                                         _ptr(sel), _ptr(w), _lists(lists), _ptr(ws), _bytes(ws), _stream(stream))
+    st = (_lib or load_library()).moe_route_scored(
+        _ptr(logits), _ptr(bias), _dims(B, 0, E, k, 0),
+        _scoring(score, groups, top_groups, group_best, int(renorm), float(scale)), _ptr(sel), _ptr(w), _lists(lists),
+        _ptr(ws), _bytes(ws), _stream_of(stream, logits))
     _check(st, "moe_route_scored")
     return sel, w, lists
 
@@ -383,15 +409,16 @@ def moe_quantize_blocks(x, block_rows: int = 1, q=None, scale=None, stream=None)
     """-> (q e4m3, scale fp32) of x[..., rows, cols] (fp32 or bf16): a
     power-of-two scale per 128 columns of a row (block_rows 1: scale[...,
     rows, ceil(cols / 128)]) or per 128 x 128 block (block_rows 128)."""
-    rows, cols = x.shape[-2:]
+    shape = x.shape
+    rows, cols = shape[-2:]
     batch = x.numel() // (rows * cols) if rows * cols else 0
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     if scale is None:
         rb = rows if block_rows == 1 else -(-rows // 128)
-        scale = torch.empty(*x.shape[:-2], rb, -(-cols // 128), dtype=torch.float32, device=x.device)
-    st = load_library().moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows, _ptr(q), _ptr(scale),
-                                            _stream(stream))
+        scale = torch.empty((*shape[:-2], rb, -(-cols // 128)), dtype=torch.float32, device=x.device)
+    st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows, _ptr(q),
+                                                      _ptr(scale), _stream_of(stream, x))
     _check(st, "moe_quantize_blocks")
     return q, scale
 
@@ -407,9 +434,9 @@ def moe_expert_gemm_blocks(q, scale, W, Wscale, lists: dict, k: int, ws=None, y=
         ws = new_gemm_workspace(q.device)
     if y is None:
         y = torch.empty(B * k, F, dtype=y_dtype, device=q.device)
-    st = load_library().moe_expert_gemm_blocks(_ptr(q), _ptr(scale), _ptr(W), _ptr(Wscale), Dims(B, d, E, k, F),
-                                               _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws),
-                                               _stream(stream))
+    st = (_lib or load_library()).moe_expert_gemm_blocks(
+        _ptr(q), _ptr(scale), _ptr(W), _ptr(Wscale), _dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws),
+        _bytes(ws), _stream_of(stream, q))
     _check(st, "moe_expert_gemm_blocks")
     return y
 
@@ -424,9 +451,9 @@ def moe_expert_ffn_blocks(x, Wgate, Sgate, Wup, Sup, Wdown, Sdown, lists: dict, 
         ws = new_blocks_workspace(B, d, E, k, F, x.device)
     if y is None:
         y = torch.empty(B, d, dtype=y_dtype or x.dtype, device=x.device)
-    st = load_library().moe_expert_ffn_blocks(
+    st = (_lib or load_library()).moe_expert_ffn_blocks(
         _ptr(x), _dtype(x), BlockWeights(_ptr(Wgate), _ptr(Sgate), _ptr(Wup), _ptr(Sup), _ptr(Wdown), _ptr(Sdown)),
-        Dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws), _stream(stream))
+        _dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws), _stream_of(stream, x))
     _check(st, "moe_expert_ffn_blocks")
     return y
 
