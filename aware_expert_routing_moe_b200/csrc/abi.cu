@@ -606,7 +606,6 @@ moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const 
         return MOE_ERR_CUDA;
     ProductArgs a = product_args(dims, lists, ws);
     a.phases = 1;
-    a.pairs = product_pairs(dims);
     ProductPhase &p = a.phase[0];
     p.kind = PRODUCT_OUT;
     p.K = dims.d;
@@ -677,19 +676,9 @@ moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weig
     st = from_cuda(launch_quantize_dispatch(x, x_type, rows, dims.d, dispatch ? lists.tok : nullptr, dims.B, xq, xs,
                                             counts, static_cast<int>(L.n_counts), s));
     if (st != MOE_OK) return st;
-    a.chained = 1;
-    a.pairs = product_pairs(dims);
-    if (a.pairs) {
-        a.phases = 1;
-        st = from_cuda(launch_product(maps, a, s));
-        if (st != MOE_OK) return st;
-        maps.phase[0] = maps.phase[1];
-        a.phase[0] = a.phase[1];
-        a.cnt = nullptr;
-    }
     st = from_cuda(launch_product(maps, a, s));
     if (st != MOE_OK) return st;
-    return from_cuda(launch_combine(yp, lists.w, counts, inv, dims.B, dims.d, dims.k, y, y_type == MOE_BF16, s));
+    return from_cuda(launch_combine(yp, lists.w, a.cnt, inv, dims.B, dims.d, dims.k, y, y_type == MOE_BF16, s));
 }
 
 void moe_set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns == 0 ? DEFAULT_WAIT_NS : ns, std::memory_order_relaxed); }

@@ -40,6 +40,7 @@ namespace {
 constexpr unsigned ALL = 0xffffffffu;
 constexpr int TILE_M = 128;       // list entries per tile
 constexpr int TILE_N = 256;       // weight rows per tile (128 + 128 for gate/up)
+constexpr int W_STAGE = TILE_N * BLK;  // weight bytes of a stage: 256 rows x 128 columns
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (EPI_WARPS + 4) * 32;
 // Registers a thread: the block starts with 168 (384 threads); the four
@@ -51,44 +52,27 @@ constexpr int OUT_STAGE = 32 * OUT_PITCH;
 constexpr int SGROUP = 4;         // column blocks whose scales are copied together (16 bytes a row)
 constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
-constexpr int PAIR_ENTRIES = 128;  // average entries of an expert from which CTAs work in pairs
 constexpr int GATHER_MAX = 32;    // rows that are gathered although they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
-// How a CTA's shared memory is laid out: AR rows of activations per stage
-// (batches of up to AR tokens: no expert has more entries).  PAIR: a cluster
-// of two CTAs shares each tile: 256 entries, 128 a CTA, by 256 weight rows,
-// of which each CTA loads 128 and the pair's MMAs (cta_group::2) read both
-// halves, so that a stage is 32 KB a CTA instead of 48.  With every expert's
-// entries filling the tiles the kernel is bound by the copies from L2 to the
-// SMs (a CTA's 48 KB stage took about 1000 cycles, its MMAs 512).
-template <int AR_, bool PAIR_>
+// Batches of up to AR tokens (no expert has more entries) keep AR rows of
+// activations per stage, which leaves room for a fifth stage.
+template <int AR>
 struct Ring {
-    static constexpr int AR = AR_;
-    static constexpr bool PAIR = PAIR_;
-    static constexpr int CTAS = PAIR ? 2 : 1;
-    static constexpr int W_STAGE = TILE_N / CTAS * BLK;  // weight bytes of a stage
     static constexpr int A_STAGE = AR * BLK;
     static constexpr int STAGE = W_STAGE + A_STAGE;
-    static constexpr int STAGES = PAIR ? 6 : AR == TILE_M ? 4 : 5;
+    static constexpr int STAGES = AR == TILE_M ? 4 : 5;
     static constexpr int OUT_STAGES = AR / 32 * 2;  // epilogue warps that can hold rows
-    static constexpr int ENTRIES = TILE_M * CTAS;   // list entries per tile
 };
-using Ring64 = Ring<64, false>;
-using Ring128 = Ring<128, false>;
-using RingPair = Ring<128, true>;
-constexpr int STAGES_MAX = 6;
 
 enum : int { TILE_END = 2 };
 struct Tile {
     int phase, e, p0, n, nb, mt;  // phase (TILE_END: no more), expert, first entry, entries, column tile, m-tile
     int ready;                    // down: its gate/up tiles were done when it was claimed
-    int box;                      // its activation rows are consecutive, and more than GATHER_MAX
 };
 
 struct Ctl {
-    unsigned long long full[STAGES_MAX], empty[STAGES_MAX];
-    unsigned long long peer_full[STAGES_MAX];  // pair: the other CTA's copies (used by the first)
+    unsigned long long full[5], empty[5];
     unsigned long long part_full[2], part_free[2];
     unsigned long long scale_full[SCALES], scale_free[SCALES];
     unsigned long long tile_full[TILES], tile_free[TILES];
@@ -107,17 +91,15 @@ struct Ctl {
     int off[SE_MAX + 1];              // first entry of a slot, its first m-tile, its expert
     uint16_t mt[SE_MAX + 1], act[SE_MAX];
 };
-template <class R>
+template <int AR>
 constexpr int smem_bytes() {
-    return 1024 + R::STAGES * R::STAGE + R::OUT_STAGES * OUT_STAGE + static_cast<int>(sizeof(Ctl));
+    return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_STAGES * OUT_STAGE + static_cast<int>(sizeof(Ctl));
 }
 static_assert(ST_MAX * K_MAX / TILE_M + SE_MAX < 65536, "m-tile numbers are 16 bits");
-static_assert(smem_bytes<Ring64>() <= 232448 - 64 && smem_bytes<Ring128>() <= 232448 - 64 &&
-                  smem_bytes<RingPair>() <= 232448 - 64,
-              "shared memory budget");
+static_assert(smem_bytes<128>() <= 232448 - 64 && smem_bytes<64>() <= 232448 - 64, "shared memory budget");
 // an MMA reads 128 activation rows: those past a 64-row region are bytes of
 // the next region (their sums are not used)
-static_assert((TILE_M - 64) * BLK <= Ring64::OUT_STAGES * OUT_STAGE, "the last stage's operand must end inside the block's memory");
+static_assert((TILE_M - 64) * BLK <= Ring<64>::OUT_STAGES * OUT_STAGE, "the last stage's operand must end inside the block's memory");
 
 // ---------------------------------------------------------------- PTX --
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -137,23 +119,6 @@ __device__ __forceinline__ void bar_arrive(unsigned long long *b) {
 }
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr(dst)), "l"(src) : "memory");
-}
-// The same barrier of CTA `rank` of the cluster.
-__device__ __forceinline__ void bar_arrive_at(unsigned long long *b, unsigned rank) {
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(saddr(b)),
-        "r"(rank)
-        : "memory");
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // four bytes global -> shared; arrive on b when this thread's copies land
 __device__ __forceinline__ void copy4(void *dst, const void *src) {
@@ -185,7 +150,7 @@ __device__ __forceinline__ bool bar_try(unsigned long long *b, unsigned parity) 
     unsigned ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(saddr(b)), "r"(parity)
@@ -226,48 +191,16 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (format code 0), fp32
-// accumulator, both K-major, M = 128 (256 for a pair), N = 256.
-template <class R>
+// accumulator, both K-major, M = 128, N = 256.
+constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE_N >> 3) << 17) |
+                           (static_cast<uint32_t>(TILE_M >> 4) << 24);
 __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE_N >> 3) << 17) |
-                               (static_cast<uint32_t>(R::ENTRIES >> 4) << 24);
-    if constexpr (R::PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
-            : "memory");
-}
-// Arrive on the barrier (of both CTAs of a pair) when the MMAs so far are done.
-template <class R>
-__device__ __forceinline__ void umma_done(unsigned long long *b) {
-    if constexpr (R::PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                saddr(b)),
-            "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else umma_commit(saddr(b));
-}
-template <class R>
-__device__ __forceinline__ void tmem_take(uint32_t dst) {
-    if constexpr (R::PAIR) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dst) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else tmem_alloc(dst, 512);
-}
-template <class R>
-__device__ __forceinline__ void tmem_give(uint32_t taddr) {
-    if constexpr (R::PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
-    else tmem_dealloc(taddr, 512);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
+        : "memory");
 }
 // 32 consecutive fp32 columns of the warp's 32 TMEM lanes; the registers
 // hold them after tmem_wait, which also waits for the loads issued before
@@ -317,7 +250,6 @@ __device__ __forceinline__ bool wait_bar(unsigned long long *b, unsigned parity,
 // column tiles, within one the m-tiles (CTAs that run together then share
 // weights in L2).  A slot without entries holds no m-tile: the search takes
 // the last slot whose first m-tile is at most t / nbt.
-template <class R>
 __device__ Tile tile_at(int t, int phase, int nbt, const Ctl *ctl) {
     int lo = 0, hi = ctl->n_slots - 1;
     const int v = t / nbt;
@@ -334,20 +266,13 @@ __device__ Tile tile_at(int t, int phase, int nbt, const Ctl *ctl) {
     x.nb = r / mts;
     const int m = r - x.nb * mts;
     x.mt = ctl->mt[lo] + m;
-    x.p0 = ctl->off[lo] + m * R::ENTRIES;
-    x.n = ctl->off[lo + 1] - x.p0;
-    if constexpr (R::PAIR) {  // the CTA's half, which may be empty
-        const int skip = min(x.n, TILE_M * static_cast<int>(cluster_rank()));
-        x.p0 += skip;
-        x.n -= skip;
-    }
-    x.n = min(TILE_M, x.n);
+    x.p0 = ctl->off[lo] + m * TILE_M;
+    x.n = min(TILE_M, ctl->off[lo + 1] - x.p0);
     return x;
 }
 
 // The call's slots from the lists, checked before anything indexes with
 // them: inconsistent lists run as an empty call and are recorded.
-template <class R>
 __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
     __shared__ int s_bad;
     const int most = min(a.E, a.B * a.k);
@@ -375,7 +300,7 @@ __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
         int run = 0;
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + threadIdx.x;
-            int v = i < n ? (ctl->off[i + 1] - ctl->off[i] + R::ENTRIES - 1) / R::ENTRIES : 0;
+            int v = i < n ? (ctl->off[i + 1] - ctl->off[i] + TILE_M - 1) / TILE_M : 0;
             const int mine = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -418,7 +343,6 @@ struct TileCursor {
 // Claims tiles ahead of the other roles (with the activation rows of their
 // entries), and publishes finished gate/up tiles: the fence before a
 // publication takes a microsecond that the epilogue does not wait for.
-template <class R>
 __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
     const int lane = threadIdx.x & 31;
     const int nbt0 = column_tiles(a.phase[0]), t0 = ctl->m_tiles * nbt0;
@@ -433,30 +357,22 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
         if (open) slot = __all_sync(ALL, claimed < TILES || bar_try(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
         if (slot) {
             int t = 0;
-            if constexpr (R::PAIR) {
-                // pairs take tiles in turn: both CTAs know them
-                t = static_cast<int>(blockIdx.x / 2 + claimed * (gridDim.x / 2));
-            } else {
-                if (lane == 0) t = atomicAdd(a.next_tile, 1);
-                t = __shfl_sync(ALL, t, 0);
-            }
+            if (lane == 0) t = atomicAdd(a.next_tile, 1);
+            t = __shfl_sync(ALL, t, 0);
             Tile x;
             x.phase = TILE_END;
-            x.n = x.ready = x.box = 0;
-            if (t < t0) x = tile_at<R>(t, 0, nbt0, ctl);
-            else if (t < total) x = tile_at<R>(t - t0, 1, nbt1, ctl);
+            x.n = x.ready = 0;
+            if (t < t0) x = tile_at(t, 0, nbt0, ctl);
+            else if (t < total) x = tile_at(t - t0, 1, nbt1, ctl);
             int tok[4];
             if (x.phase != TILE_END) {
                 const bool by_pair = a.phase[x.phase].by_pair != 0;
-                bool run = true;
-                int first = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     // rows past the tile's end repeat its last one (their sums are not used)
-                    const int p = x.p0 + max(min(lane + 32 * q, x.n - 1), 0);
+                    const int p = x.p0 + min(lane + 32 * q, x.n - 1);
                     int r = p;
-                    tok[q] = -1;
-                    if (x.n > 0 && (!by_pair || (x.phase == 0 && a.cnt != nullptr))) {
+                    if (!by_pair || x.phase == 0) {
                         tok[q] = __ldg(a.tok + p);
                         if (tok[q] < 0 || tok[q] >= a.B) {
                             atomicCAS(a.error, 0, DEV_BAD_LISTS);
@@ -465,10 +381,7 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
                         if (!by_pair) r = max(tok[q], 0);
                     }
                     ctl->rows[s][lane + 32 * q] = r;
-                    if (q == 0) first = __shfl_sync(ALL, r, 0);
-                    run = run && r == first + max(min(lane + 32 * q, x.n - 1), 0);
                 }
-                x.box = __all_sync(ALL, run) && x.n > GATHER_MAX;
                 if (x.phase == 1) {
                     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are zero
                     waited = true;
@@ -480,8 +393,8 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
             if (lane == 0) bar_arrive(&ctl->tile_full[s]);
             ++claimed;
             open = x.phase != TILE_END;
-            if (x.phase == 0 && a.cnt != nullptr) {
-                if (a.phases > 1) ++to_publish;
+            if (a.phases > 1 && x.phase == 0) {
+                ++to_publish;
                 if (x.nb == 0) {  // the entries of each token, for the combine
                     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
                     waited = true;
@@ -535,21 +448,15 @@ __device__ void drain_fills(Ctl *ctl) {
         }
 }
 
-template <class R>
+template <int AR>
 __device__ unsigned weights_role(unsigned char *ring, Ctl *ctl, const ProductMaps &maps, const ProductArgs &a) {
+    using R = Ring<AR>;
     TileCursor cur;
     Tile x;
     unsigned it = 0;
-    bool second = false, waited = false;
-    if constexpr (R::PAIR) second = cluster_rank() != 0;
     while (cur.next(ctl, a, x)) {
-        const int first = ctl->rows[cur.i % TILES][0];
         cur.release(ctl);
         if (x.phase == TILE_END) return it;
-        if (R::PAIR && !waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are the previous kernel's
-            waited = true;
-        }
         const ProductPhase &ph = a.phase[x.phase];
         const int kb = (ph.K + BLK - 1) / BLK;
         const int r0 = ph.kind == PRODUCT_SWIGLU ? x.nb * BLK : x.nb * TILE_N;
@@ -560,37 +467,23 @@ __device__ unsigned weights_role(unsigned char *ring, Ctl *ctl, const ProductMap
             unsigned char *w = ring + st * R::STAGE;
             if (it >= R::STAGES && !wait_bar(&ctl->empty[st], (it / R::STAGES - 1) & 1, ctl, a, DEV_TIMEOUT_EMPTY))
                 return it;
-            bar_expect(&ctl->full[st], R::W_STAGE);
-            if constexpr (R::PAIR) {
-                load_box(w, second ? m1 : m0, j * BLK, second ? r1 : r0, x.e, &ctl->full[st]);
-                if (x.box) {  // the rows too: this thread's loop is the shortest
-                    bar_expect(&ctl->full[st], R::A_STAGE);
-                    load_rows(w + R::W_STAGE, &maps.phase[0].ab, j * BLK, first, &ctl->full[st]);
-                }
-            } else {
-                load_box(w, m0, j * BLK, r0, x.e, &ctl->full[st]);
-                load_box(w + R::W_STAGE / 2, m1, j * BLK, r1, x.e, &ctl->full[st]);
-            }
+            bar_expect(&ctl->full[st], W_STAGE);
+            load_box(w, m0, j * BLK, r0, x.e, &ctl->full[st]);
+            load_box(w + W_STAGE / 2, m1, j * BLK, r1, x.e, &ctl->full[st]);
         }
     }
     return it;
 }
 
-template <class R>
+template <int AR>
 __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &maps, const ProductArgs &a) {
+    using R = Ring<AR>;
     const int lane = threadIdx.x & 31;
     TileCursor cur;
     Tile x;
     unsigned it = 0, sg = 0;
     int st = 0;
     unsigned phase = 0;  // of stage st's present fill
-    auto advance = [&] {
-        ++it;
-        if (++st == R::STAGES) {
-            st = 0;
-            phase ^= 1;
-        }
-    };
     // the activations are the previous kernel's
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (;;) {
@@ -635,7 +528,10 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
         const bool wide = (ph.as_pitch & 3) == 0;
         // consecutive rows in one box; few rows, or scattered ones, four at a time
         const int first = __shfl_sync(ALL, rows[0], 0);
-        const bool box = x.box != 0;
+        bool run = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) run = run && rows[q] == first + min(lane * 4 + q, x.n - 1);
+        const bool box = __all_sync(ALL, run) && x.n > GATHER_MAX;
         const int groups = (x.n + 3) >> 2;
         const unsigned bytes = box ? R::A_STAGE : groups * 4 * BLK;
         const CUtensorMap *m = box ? &maps.phase[x.phase].ab : &maps.phase[x.phase].a;
@@ -658,26 +554,27 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
                 copies_arrive(&ctl->scale_full[sc]);
                 ++sg;
             }
-            if (R::PAIR && box) {  // loaded with the weights
-                advance();
-                continue;
-            }
             unsigned long long *full = &ctl->full[st];
             if (it >= R::STAGES && !__all_sync(ALL, wait_bar(&ctl->empty[st], phase ^ 1, ctl, a, DEV_TIMEOUT_EMPTY))) return it;
             if (lane == 0) bar_expect(full, bytes);
             __syncwarp();
             if (mine) {
-                unsigned char *d = ring + st * R::STAGE + R::W_STAGE;
+                unsigned char *d = ring + st * R::STAGE + W_STAGE;
                 if (box) load_rows(d, m, j * BLK, first, full);
                 else load_rows4(d + lane * 4 * BLK, m, j * BLK, rows, full);
             }
-            advance();
+            ++it;
+            if (++st == R::STAGES) {
+                st = 0;
+                phase ^= 1;
+            }
         }
     }
 }
 
-template <class R>
+template <int AR>
 __device__ void issue_role(unsigned char *ring, Ctl *ctl, const ProductArgs &a) {
+    using R = Ring<AR>;
     const uint32_t tmem = ctl->tmem;
     TileCursor cur;
     Tile x;
@@ -688,26 +585,16 @@ __device__ void issue_role(unsigned char *ring, Ctl *ctl, const ProductArgs &a) 
         const int kb = (a.phase[x.phase].K + BLK - 1) / BLK;
         for (int j = 0; j < kb; ++j, ++it) {
             const int st = it % R::STAGES, buf = it & 1;
-            if constexpr (R::PAIR) {
-                // the second CTA only tells the first that its copies landed
-                if (cluster_rank() != 0) {
-                    if (!wait_bar(&ctl->full[st], (it / R::STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return;
-                    bar_arrive_at(&ctl->peer_full[st], 0);
-                    continue;
-                }
-            }
             if (it >= 2 && !wait_bar(&ctl->part_free[buf], ((it >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP)) return;
             if (!wait_bar(&ctl->full[st], (it / R::STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return;
-            if constexpr (R::PAIR)
-                if (!wait_bar(&ctl->peer_full[st], (it / R::STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return;
             tc_fence_after();
             const uint64_t b = umma_desc(saddr(ring + st * R::STAGE));
-            const uint64_t v = umma_desc(saddr(ring + st * R::STAGE + R::W_STAGE));
+            const uint64_t v = umma_desc(saddr(ring + st * R::STAGE + W_STAGE));
 #pragma unroll
             for (int s = 0; s < 4; ++s)  // 32 columns = 32 bytes each
-                umma_e4m3<R>(tmem + buf * TILE_N, v + 2 * s, b + 2 * s, s > 0);
-            umma_done<R>(&ctl->empty[st]);
-            umma_done<R>(&ctl->part_full[buf]);
+                umma_e4m3(tmem + buf * TILE_N, v + 2 * s, b + 2 * s, s > 0);
+            umma_commit(saddr(&ctl->empty[st]));
+            umma_commit(saddr(&ctl->part_full[buf]));
         }
     }
 }
@@ -787,20 +674,13 @@ __device__ __forceinline__ void store_out(unsigned char *stage, const float (&c)
     }
 }
 
-// The warp has read a TMEM buffer: tell the issuer.
-template <class R>
-__device__ __forceinline__ void part_read(Ctl *ctl, int buf) {
-    if constexpr (R::PAIR) bar_arrive_at(&ctl->part_free[buf], 0);
-    else bar_arrive(&ctl->part_free[buf]);
-}
-
-template <class R>
+template <int AR>
 __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .., columns 64 half .. of each matrix
     const int row = quarter * 32 + lane;
     const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
-    unsigned char *stage = out_stage + (half * (R::AR / 32) + quarter) * OUT_STAGE;  // used by warps with rows
+    unsigned char *stage = out_stage + (half * (AR / 32) + quarter) * OUT_STAGE;  // used by warps with rows
     bool dead = false;
     unsigned it = 0, gu = 0, sg = 0;
     TileCursor cur;
@@ -849,7 +729,7 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    part_read<R>(ctl, buf);
+                    bar_arrive(&ctl->part_free[buf]);
                     if (last) bar_arrive(&ctl->scale_free[sc]);
                 }
                 add32(c1 + 32, v, m1);
@@ -857,7 +737,7 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    part_read<R>(ctl, buf);
+                    bar_arrive(&ctl->part_free[buf]);
                     if (last) bar_arrive(&ctl->scale_free[sc]);
                 }
             }
@@ -895,7 +775,6 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                 if (row < x.n && half == 0)
                     ph.hs[static_cast<size_t>(x.p0 + row) * ph.hs_pitch + x.nb] = __int_as_float((127 + e) << 23);
             }
-            if (a.phases == 1) continue;  // the down product is a launch of its own
             const int slot = gu & 1;
             if (gu >= 2 && !dead) dead = !__all_sync(ALL, wait_bar(&ctl->pub_free[slot], ((gu >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP));
             ++gu;
@@ -910,9 +789,10 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
     }
 }
 
-template <class R>
+template <int AR>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductMaps maps,
                                                              const __grid_constant__ ProductArgs a) {
+    using R = Ring<AR>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -923,11 +803,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         for (int i = 0; i < R::STAGES; ++i) {
             bar_init(&ctl->full[i], 2);  // weights and rows
             bar_init(&ctl->empty[i], 1);
-            bar_init(&ctl->peer_full[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&ctl->part_full[i], 1);
-            bar_init(&ctl->part_free[i], EPI_WARPS * R::CTAS);
+            bar_init(&ctl->part_free[i], EPI_WARPS);
         }
         for (int i = 0; i < SCALES; ++i) {
             bar_init(&ctl->scale_full[i], 32);
@@ -946,54 +825,50 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         ctl->abort_flag = 0;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == EPI_WARPS + 1) tmem_take<R>(saddr(&ctl->tmem));
+    if (warp == EPI_WARPS + 1) tmem_alloc(saddr(&ctl->tmem), 512);
     tc_fence_before();
-    build_slots<R>(ctl, a);  // ends in a block barrier
-    if constexpr (R::PAIR) cluster_sync();  // both CTAs' barriers are set up
+    build_slots(ctl, a);  // ends in a block barrier
     tc_fence_after();
     if (warp < EPI_WARPS) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
-        epilogue_role<R>(out_stage, ctl, a);
+        epilogue_role<AR>(out_stage, ctl, a);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
         if (warp == EPI_WARPS) {
-            if (elect_one()) ctl->fills[0] = weights_role<R>(ring, ctl, maps, a);
+            if (elect_one()) ctl->fills[0] = weights_role<AR>(ring, ctl, maps, a);
         } else if (warp == EPI_WARPS + 1) {
             if (elect_one()) {
-                issue_role<R>(ring, ctl, a);
-                bool first = true;  // the CTA that issues the MMAs
-                if constexpr (R::PAIR) first = cluster_rank() == 0;
-                if (first) umma_done<R>(&ctl->mma_done);
+                issue_role<AR>(ring, ctl, a);
+                umma_commit(saddr(&ctl->mma_done));
                 const unsigned long long t0 = cycles();
                 while (!bar_try(&ctl->mma_done, 0) && cycles() - t0 < DRAIN_CYCLES) {
                 }
             }
         } else if (warp == EPI_WARPS + 2) {
-            const unsigned n = rows_role<R>(ring, ctl, maps, a);
+            const unsigned n = rows_role<AR>(ring, ctl, maps, a);
             if ((threadIdx.x & 31) == 0) ctl->fills[1] = n;
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            scheduler<R>(ctl, a);
+            scheduler(ctl, a);
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (R::PAIR) cluster_sync();  // neither CTA leaves while the other may reach into it
     tc_fence_after();
-    if (warp == EPI_WARPS + 1) tmem_give<R>(ctl->tmem);
+    if (warp == EPI_WARPS + 1) tmem_dealloc(ctl->tmem, 512);
     if (threadIdx.x == 0) {
         drain_fills<R::STAGES>(ctl);
         __threadfence();
-        if (!R::PAIR && atomicAdd(a.exits, 1) == static_cast<int>(gridDim.x) - 1) {
+        if (atomicAdd(a.exits, 1) == static_cast<int>(gridDim.x) - 1) {
             *a.next_tile = 0;
             *a.exits = 0;
         }
     }
 }
 
-template <class R>
-cudaError_t launch_ring(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
+template <int AR>
+cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
     // per device: the SM count, and the shared-memory attribute set
     static int sms[MAX_DEVICES] = {};
     int dev = 0;
@@ -1004,40 +879,30 @@ cudaError_t launch_ring(const ProductMaps &maps, const ProductArgs &a, cudaStrea
         int n = 0;
         err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (err != cudaSuccess) return err;
-        err = cudaFuncSetAttribute(product_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<R>());
+        err = cudaFuncSetAttribute(product_kernel<AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<AR>());
         if (err != cudaSuccess) return err;
         sms[dev] = n;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms[dev]);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<R>();
+    cfg.dynamicSmemBytes = smem_bytes<AR>();
     cfg.stream = s;
     // after the quantisation kernel: claim tiles and stream weights meanwhile
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = a.chained;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = R::CTAS;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (R::PAIR) cfg.gridDim.x = sms[dev] / 2 * 2;
-    return cudaLaunchKernelEx(&cfg, product_kernel<R>, maps, a);
+    cfg.numAttrs = a.phases > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, product_kernel<AR>, maps, a);
 }
 
 }  // namespace
 
 int product_box_rows(int B) { return B <= 64 ? 64 : TILE_M; }
 
-bool product_pairs(const moe_dims_t &d) {
-    const long long pairs = static_cast<long long>(d.B) * d.k, experts = d.E < pairs ? d.E : pairs;
-    return d.B > TILE_M && pairs >= PAIR_ENTRIES * experts;
-}
-
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
-    if (a.pairs) return launch_ring<RingPair>(maps, a, s);
-    return a.B <= 64 ? launch_ring<Ring64>(maps, a, s) : launch_ring<Ring128>(maps, a, s);
+    return a.B <= 64 ? launch_ar<64>(maps, a, s) : launch_ar<128>(maps, a, s);
 }
 
 }  // namespace moe

@@ -70,17 +70,13 @@ struct ProductPhase {
 struct ProductArgs {
     ProductPhase phase[2];
     int phases;
-    int pairs;            // CTAs in pairs (product_pairs; one phase then)
-    int chained;          // launched dependent on the kernel before it
     int B, E, k;          // dims of the lists
     const int32_t *n_active, *active, *offsets, *tok;
     int32_t *done;        // two phases: gate/up tiles done per m-tile
-    int32_t *cnt, *inv;   // gate/up (or null): entries of each token: counts [B], entry indices [B][k]
+    int32_t *cnt, *inv;   // two phases: entries of each token: counts [B], entry indices [B][k]
     int32_t *error, *next_tile, *exits;
     unsigned long long wait_ns;
 };
-// Whether a call runs on pairs of CTAs, its phases as launches of their own.
-bool product_pairs(const moe_dims_t &d);
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s);
 
 // e4m3 values and power-of-two scales of [batch][rows][cols] (block_rows 1
