@@ -22,8 +22,8 @@
 // started.  The last CTA puts the counters back to zero.
 //
 // Roles: warps 0-7 epilogue; warp 8 weights (TMA boxes; they do not wait for
-// the tile's activations); warp 9 MMAs; warp 10 activation rows (a box, or
-// gathered four at a time by list entry) and the scales of each column
+// the tile's activations); warp 9 MMAs; warp 10 activation rows (boxes of
+// 32 where they are consecutive, else gathered four at a time) and the scales of each column
 // block, copied to a ring of their own, so that no global load latency sits
 // in the epilogue's loop; warp 11 claims tiles and
 // publishes finished ones.  Every wait is bounded; past
@@ -52,7 +52,7 @@ constexpr int OUT_STAGE = 32 * OUT_PITCH;
 constexpr int SGROUP = 4;         // column blocks whose scales are copied together (16 bytes a row)
 constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
-constexpr int GATHER_MAX = 32;    // rows that are gathered although they are consecutive
+constexpr int BOX_ROWS = 32;      // activation rows per copy where they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
 // Batches of up to AR tokens (no expert has more entries) keep AR rows of
@@ -526,16 +526,15 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
         const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + (lane >> 2), rb - 1);
         const float *wsrc = (lane < 4 ? ph.bs0 : ph.bs1) + (static_cast<size_t>(x.e) * rb + nb) * kb;
         const bool wide = (ph.as_pitch & 3) == 0;
-        // consecutive rows in one box; few rows, or scattered ones, four at a time
+        // consecutive rows in boxes of BOX_ROWS, scattered ones four at a time
         const int first = __shfl_sync(ALL, rows[0], 0);
         bool run = true;
 #pragma unroll
         for (int q = 0; q < 4; ++q) run = run && rows[q] == first + min(lane * 4 + q, x.n - 1);
-        const bool box = __all_sync(ALL, run) && x.n > GATHER_MAX;
-        const int groups = (x.n + 3) >> 2;
-        const unsigned bytes = box ? R::A_STAGE : groups * 4 * BLK;
+        const bool box = __all_sync(ALL, run);
+        const int copies = box ? (x.n + BOX_ROWS - 1) / BOX_ROWS : (x.n + 3) >> 2;
+        const unsigned copy_bytes = box ? BOX_ROWS * BLK : 4 * BLK, bytes = copies * copy_bytes;
         const CUtensorMap *m = box ? &maps.phase[x.phase].ab : &maps.phase[x.phase].a;
-        const bool mine = box ? lane == 0 : lane < groups;
         for (int j = 0; j < kb; ++j) {
             if (j % SGROUP == 0) {
                 const unsigned sc = sg % SCALES;
@@ -558,10 +557,10 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
             if (it >= R::STAGES && !__all_sync(ALL, wait_bar(&ctl->empty[st], phase ^ 1, ctl, a, DEV_TIMEOUT_EMPTY))) return it;
             if (lane == 0) bar_expect(full, bytes);
             __syncwarp();
-            if (mine) {
-                unsigned char *d = ring + st * R::STAGE + W_STAGE;
-                if (box) load_rows(d, m, j * BLK, first, full);
-                else load_rows4(d + lane * 4 * BLK, m, j * BLK, rows, full);
+            if (lane < copies) {
+                unsigned char *d = ring + st * R::STAGE + W_STAGE + lane * copy_bytes;
+                if (box) load_rows(d, m, j * BLK, first + lane * BOX_ROWS, full);
+                else load_rows4(d, m, j * BLK, rows, full);
             }
             ++it;
             if (++st == R::STAGES) {
@@ -899,7 +898,7 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
 
 }  // namespace
 
-int product_box_rows(int B) { return B <= 64 ? 64 : TILE_M; }
+int product_box_rows() { return BOX_ROWS; }
 
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
     return a.B <= 64 ? launch_ar<64>(maps, a, s) : launch_ar<128>(maps, a, s);

@@ -48,7 +48,7 @@ struct PhaseMaps {
 struct ProductMaps {
     PhaseMaps phase[2];
 };
-int product_box_rows(int B);
+int product_box_rows();
 bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
                        uint64_t E, uint64_t rows, uint64_t K);
 

@@ -133,7 +133,8 @@ def _gemm_case(B, d, E, k, F, y_dtype, empty=0.0, few=0, seed=0):
 @pytest.mark.parametrize("y_dtype", [F32, BF16])
 @pytest.mark.parametrize("B,d,E,k,F", [
     (1, 16, 1, 1, 16), (1, 128, 4, 2, 128), (3, 272, 5, 3, 400), (33, 1040, 8, 4, 272), (129, 256, 3, 2, 256),
-    (300, 512, 2, 1, 640), (130, 144, 1, 1, 1040), (5, 4096, 16, 8, 144)])
+    (300, 512, 2, 1, 640), (130, 144, 1, 1, 1040), (5, 4096, 16, 8, 144), (600, 1040, 3, 2, 400),
+    (1000, 128, 1, 1, 4096), (257, 272, 2, 2, 16)])
 def test_gemm(B, d, E, k, F, y_dtype):
     worst = _gemm_case(B, d, E, k, F, y_dtype)
     print(f"relative error {worst:.2e}")
@@ -171,7 +172,7 @@ def _check_ffn(y, x, L, vals, what=""):
 @pytest.mark.parametrize("x_dtype,y_dtype", [(BF16, BF16), (F32, F32)])
 @pytest.mark.parametrize("B,d,E,k,F", [
     (1, 16, 1, 1, 16), (1, 256, 4, 2, 128), (4, 272, 6, 3, 144), (17, 512, 8, 4, 256), (130, 256, 2, 2, 272),
-    (40, 1040, 40, 5, 400), (300, 128, 3, 1, 128)])
+    (40, 1040, 40, 5, 400), (300, 128, 3, 1, 128), (700, 512, 4, 2, 384), (260, 272, 1, 1, 144)])
 def test_ffn(B, d, E, k, F, x_dtype, y_dtype):
     L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, x_dtype)
     ws = moe.new_blocks_workspace(B, d, E, k, F)
@@ -189,6 +190,25 @@ def test_ffn_empty_tokens():
     _check_ffn(y, x, L, vals)
     alone = np.setdiff1d(np.arange(21), L["tok"][:L["offsets"][-1]])
     assert len(alone) and torch.all(y[torch.from_numpy(alone).cuda()] == 0)
+
+
+def test_skewed_batches():
+    # most tokens on few experts, the rest with a handful each: tiles of every
+    # fill, with and without an empty half
+    rng = np.random.default_rng(5)
+    B, d, E, k, F = 500, 256, 6, 2, 256
+    sel = np.full((B, k), -1, np.int32)
+    sel[:, 0] = np.where(np.arange(B) < 300, 1, 4)
+    sel[::7, 1] = 2
+    sel[3, 1], sel[480, 1] = 0, 5
+    w = np.where(sel >= 0, rng.random((B, k)) + 0.1, 0.0).astype(np.float32)
+    L, dev = _lists(sel, w, E)
+    x = torch.from_numpy(rng.standard_normal((B, d)).astype(np.float32)).cuda()
+    mats = [_weights(rng, E, F, d), _weights(rng, E, F, d), _weights(rng, E, d, F)]
+    ws = moe.new_blocks_workspace(B, d, E, k, F)
+    y = moe.moe_expert_ffn_blocks(x, *[t for m in mats for t in m[:2]], dev, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, [m[2] for m in mats])
 
 
 def test_ffn_no_entries_is_zero():
