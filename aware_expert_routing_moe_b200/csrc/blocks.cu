@@ -157,6 +157,18 @@ __device__ __forceinline__ bool bar_try(unsigned long long *b, unsigned parity) 
         : "memory");
     return ok != 0;
 }
+// The same without the wait that try_wait may take before it says no.
+__device__ __forceinline__ bool bar_test(unsigned long long *b, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int c, int r, int e,
                                          unsigned long long *bar) {
     asm volatile(
@@ -354,7 +366,7 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
         bool idle = true;
         const int s = claimed % TILES;
         bool slot = false;
-        if (open) slot = __all_sync(ALL, claimed < TILES || bar_try(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
+        if (open) slot = __all_sync(ALL, claimed < TILES || bar_test(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
         if (slot) {
             int t = 0;
             if (lane == 0) t = atomicAdd(a.next_tile, 1);
@@ -410,7 +422,7 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
             }
             idle = false;
         }
-        if (published < to_publish && __all_sync(ALL, bar_try(&ctl->pub_full[published & 1], (published >> 1) & 1))) {
+        if (published < to_publish && __all_sync(ALL, bar_test(&ctl->pub_full[published & 1], (published >> 1) & 1))) {
             if (lane == 0) {
                 const int mt = ctl->pub_mt[published & 1];
                 // h and its scales, written by the epilogue's threads, are in

@@ -18,6 +18,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
+constexpr long long WIDE_ROWS = 2048;
 
 // Exponent e of the scale 2^e for a block whose largest magnitude is top
 // (its fp32 bits): top = m 2^(x-127), 1 <= m < 2; 448 = 1.75 * 2^8, so
@@ -89,12 +90,13 @@ struct Lane16<__nv_bfloat16> {
     }
 };
 
-// A warp per 512 columns of a row: 16 columns a lane (16-byte loads and one
-// 16-byte store), eight lanes a block of 128.  Scale of row r, block j at
+// A warp per SPAN * 512 columns of a row: 16 columns a lane and chunk of 512
+// (16-byte loads and one 16-byte store), eight lanes a block of 128, the
+// chunks' loads in flight together.  Scale of row r, block j at
 // scale[r * pitch + j].
-template <typename T>
+template <typename T, int SPAN>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, unsigned rows, int cols,
-                                                            unsigned chunks, const int32_t *__restrict__ src, int n_src,
+                                                            unsigned spans, const int32_t *__restrict__ src, int n_src,
                                                             uint8_t *__restrict__ q, float *__restrict__ scale,
                                                             int pitch, int32_t *__restrict__ zero, int n_zero) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -102,25 +104,32 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
     const unsigned warps = gridDim.x * 8;
     if (zero != nullptr)
         for (int i = blockIdx.x * 256 + threadIdx.x; i < n_zero; i += gridDim.x * 256) zero[i] = 0;
-    const unsigned items = rows * chunks;
+    const unsigned items = rows * spans;
     for (unsigned b = blockIdx.x * 8 + (threadIdx.x >> 5); b < items; b += warps) {
-        const unsigned r = b / chunks;
-        const int c = static_cast<int>(b - r * chunks) * 512 + lane * 16;
+        const unsigned r = b / spans;
+        const int c0 = static_cast<int>(b - r * spans) * SPAN * 512 + lane * 16;
         long long from = r;
         if (src != nullptr) {
             from = __ldg(src + r);
             if (from < 0 || from >= n_src) continue;  // past the last entry (or a bad list, reported by the product)
         }
-        Lane16<T> v;
-        if (c < cols) v.load(x + from * cols + c);
-        else v.zero();
-        unsigned top = v.top();
+        Lane16<T> v[SPAN];
 #pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(ALL, top, o));
-        const int e = scale_exp(top);
-        if (c < cols) {
-            *reinterpret_cast<uint4 *>(q + static_cast<long long>(r) * cols + c) = v.pack(pow2(-e));
-            if ((lane & 7) == 0) scale[static_cast<long long>(r) * pitch + c / BLK] = pow2(e);
+        for (int u = 0; u < SPAN; ++u) {
+            if (c0 + u * 512 < cols) v[u].load(x + from * cols + c0 + u * 512);
+            else v[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < SPAN; ++u) {
+            const int c = c0 + u * 512;
+            unsigned top = v[u].top();
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(ALL, top, o));
+            const int e = scale_exp(top);
+            if (c < cols) {
+                *reinterpret_cast<uint4 *>(q + static_cast<long long>(r) * cols + c) = v[u].pack(pow2(-e));
+                if ((lane & 7) == 0) scale[static_cast<long long>(r) * pitch + c / BLK] = pow2(e);
+            }
         }
         if (b + warps < b) break;  // the counter would wrap
     }
@@ -207,18 +216,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
 }  // namespace
 
 namespace {
+template <typename T, int SPAN>
+cudaError_t launch_span(const void *x, long long rows, int cols, const int32_t *src, int n_src, uint8_t *q, float *scale,
+                        int pitch, int32_t *zero, int n_zero, cudaStream_t s) {
+    const unsigned spans = (cols + SPAN * 512 - 1) / (SPAN * 512);
+    const long long blocks = (rows * spans + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
+    quantize_rows_kernel<T, SPAN><<<grid, 256, 0, s>>>(static_cast<const T *>(x), static_cast<unsigned>(rows), cols, spans,
+                                                       src, n_src, q, scale, pitch, zero, n_zero);
+    return cudaGetLastError();
+}
 cudaError_t launch_rows(const void *x, int type, long long rows, int cols, const int32_t *src, int n_src, uint8_t *q,
                         float *scale, int pitch, int32_t *zero, int n_zero, cudaStream_t s) {
-    const unsigned chunks = (cols + 511) / 512, n = static_cast<unsigned>(rows);
-    const long long blocks = (rows * chunks + 7) / 8;
-    const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
+    // many rows: the row index (and the gathered row's) once for 1024 or
+    // 2048 columns; few: as many warps as there are chunks
+    const bool many = rows >= WIDE_ROWS;
     if (type == MOE_BF16)
-        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), n, cols, chunks, src, n_src, q,
-                                                  scale, pitch, zero, n_zero);
-    else
-        quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(x), n, cols, chunks, src, n_src, q, scale,
-                                                  pitch, zero, n_zero);
-    return cudaGetLastError();
+        return many ? launch_span<__nv_bfloat16, 4>(x, rows, cols, src, n_src, q, scale, pitch, zero, n_zero, s)
+                    : launch_span<__nv_bfloat16, 1>(x, rows, cols, src, n_src, q, scale, pitch, zero, n_zero, s);
+    return many ? launch_span<float, 2>(x, rows, cols, src, n_src, q, scale, pitch, zero, n_zero, s)
+                : launch_span<float, 1>(x, rows, cols, src, n_src, q, scale, pitch, zero, n_zero, s);
 }
 }  // namespace
 
