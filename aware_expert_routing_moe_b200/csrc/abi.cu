@@ -198,6 +198,7 @@ ProductArgs product_args(const moe_dims_t &d, const moe_lists_t &l, void *ws) {
     a.next_tile = &c->next_tile;
     a.exits = &c->exits;
     a.wait_ns = wait_limit_ns();
+    a.tile_entries = product_tile_entries(d);
     return a;
 }
 
@@ -317,8 +318,8 @@ BlocksWs blocks_ws(const moe_dims_t &d) {
     w.hq = o;  o += round_up(P * F);
     w.hs = o;  o += round_up(P * scale_pitch(d.d_ff) * 4);
     w.yp = o;  o += round_up(P * D * 4);
-    // m-tiles: one per 128 entries, and a short one per active expert at most
-    w.n_counts = B + (P / 128 + (E < P ? E : P));
+    // m-tiles: the full ones, and a short one per active expert at most
+    w.n_counts = B + (P / product_tile_entries(d) + (E < P ? E : P));
     w.counts = o; o += round_up(w.n_counts * 4);
     w.inv = o; o += round_up(P * 4);
     w.total = o;

@@ -2,17 +2,23 @@
 // e4m3 operands, one fp32 scale per 128 columns of an activation row and per
 // 128 x 128 block of a weight matrix, on the 5th-generation tensor cores.
 //
-// A tile is up to 128 list entries of one expert (the MMA's M, TMEM lanes)
-// by 256 weight rows (its N): for a plain product 256 rows of W, for the
-// gate/up product 128 rows of Wgate and the same 128 of Wup.  Scales change
-// every 128 columns, so the sum over a column block is formed in TMEM by
-// four MMAs of K = 32 and added, times the row's and the block's scale, to
-// fp32 accumulators in registers: thread (row, column half) of the eight
-// epilogue warps holds 128 of the row's 256 sums.  With the entries on the
-// lanes a row's scale is one register, and SwiGLU, the largest magnitude of
-// a block of h and its rounding to e4m3 stay inside a thread (two threads
-// share a block).  Two TMEM buffers of 256 columns let the MMAs of the next
-// column block run while one is added.
+// A tile is some list entries of one expert by 256 weight rows: for a plain
+// product 256 rows of W, for the gate/up product 128 rows of Wgate and the
+// same 128 of Wup.  Scales change every 128 columns, so the sum over a column
+// block is formed in TMEM by MMAs of K = 32 and added, times the row's and
+// the block's scale, to fp32 accumulators in the registers of eight epilogue
+// warps; several TMEM buffers let the MMAs of the next blocks run meanwhile.
+//
+// Few entries (up to 64 a tile): the weights are the MMA's M (two MMAs of
+// 128 rows), the entries its N (16 to 64).  An MMA then costs what its
+// entries cost: with the entries as a half-empty M of 128 the decode kernels
+// drew 990 W and lost a sixth of their speed to the power cap (8 tokens,
+// Qwen3-235B shape, back to back: 174 us against 150 in a short run).  A
+// thread holds one weight row of both matrices for up to 32 entries.
+// Many entries (up to 128 a tile): the entries are M (TMEM lanes), the 256
+// weight rows N.  An entry's scale is then one register, and SwiGLU, the
+// largest magnitude of a block of h and its rounding to e4m3 stay inside a
+// thread: thread (entry, column half) holds 128 of the entry's 256 sums.
 //
 // A call is one phase (a plain product) or two (gate/up, then down, whose
 // activations are the first phase's h).  Persistent CTAs, one per SM, claim
@@ -38,13 +44,14 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
-constexpr int TILE_M = 128;       // list entries per tile
+constexpr int TILE_MANY = 128, TILE_FEW = 64;  // list entries per tile
 constexpr int TILE_N = 256;       // weight rows per tile (128 + 128 for gate/up)
 constexpr int W_STAGE = TILE_N * BLK;  // weight bytes of a stage: 256 rows x 128 columns
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (EPI_WARPS + 4) * 32;
-// Registers a thread: the block starts with 168 (384 threads); the four
-// copy and issue warps give theirs up for the epilogue's accumulators.
+// Registers a thread: the block starts with 168 (384 threads); with many
+// entries the four copy and issue warps give theirs up for the epilogue's
+// accumulators.
 constexpr int REGS_EPI = 224, REGS_COPY = 56;
 static_assert(256 * REGS_EPI + 128 * REGS_COPY <= THREADS * 168, "register split");
 constexpr int OUT_PITCH = 80;     // bytes of a staged output row: 64 and a pad that spreads the banks
@@ -52,17 +59,21 @@ constexpr int OUT_STAGE = 32 * OUT_PITCH;
 constexpr int SGROUP = 4;         // column blocks whose scales are copied together (16 bytes a row)
 constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
+constexpr int FEW_ENTRIES = 48;   // an expert's entries, on average, up to which tiles are of 64
 constexpr int BOX_ROWS = 32;      // activation rows per copy where they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
-// Batches of up to AR tokens (no expert has more entries) keep AR rows of
-// activations per stage, which leaves room for a fifth stage.
+// A kernel for tiles of AR entries: AR activation rows per stage; with few
+// entries a fifth stage fits, and four TMEM buffers.
 template <int AR>
 struct Ring {
+    static constexpr bool FEW = AR == TILE_FEW;
     static constexpr int A_STAGE = AR * BLK;
     static constexpr int STAGE = W_STAGE + A_STAGE;
-    static constexpr int STAGES = AR == TILE_M ? 4 : 5;
-    static constexpr int OUT_STAGES = AR / 32 * 2;  // epilogue warps that can hold rows
+    static constexpr int STAGES = FEW ? 5 : 4;
+    static constexpr int OUT_BYTES = FEW ? AR * BLK : EPI_WARPS * OUT_STAGE;  // h of a tile, or a piece a warp
+    static constexpr int BUFS = FEW ? 4 : 2;          // TMEM buffers
+    static constexpr int BUF_COLS = 512 / BUFS;       // two blocks of 64 entries, or 256 weight rows
 };
 
 enum : int { TILE_END = 2 };
@@ -73,7 +84,7 @@ struct Tile {
 
 struct Ctl {
     unsigned long long full[5], empty[5];
-    unsigned long long part_full[2], part_free[2];
+    unsigned long long part_full[4], part_free[4];
     unsigned long long scale_full[SCALES], scale_free[SCALES];
     unsigned long long tile_full[TILES], tile_free[TILES];
     unsigned long long pub_full[2], pub_free[2];
@@ -83,24 +94,20 @@ struct Ctl {
     unsigned fills[2];  // stages filled with weights, with rows
     uint32_t tmem;
     Tile tile[TILES];
-    int rows[TILES][TILE_M];          // activation row of each entry of a claimed tile
+    int rows[TILES][TILE_MANY];          // activation row of each entry of a claimed tile
     int pub_mt[2];                    // m-tile of a finished gate/up tile
-    float4 scale[SCALES][TILE_M];     // each row's scales of a group of column blocks
+    float4 scale[SCALES][TILE_MANY];     // each row's scales of a group of column blocks
     float wscale[SCALES][2][SGROUP];  // and the two weight blocks'
-    float top[2][TILE_M];             // [column half][row]: largest |h|
+    float top[4][TILE_MANY];          // largest |h|: [column half][entry], few entries: [quarter of the rows][entry]
     int off[SE_MAX + 1];              // first entry of a slot, its first m-tile, its expert
     uint16_t mt[SE_MAX + 1], act[SE_MAX];
 };
 template <int AR>
 constexpr int smem_bytes() {
-    return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_STAGES * OUT_STAGE + static_cast<int>(sizeof(Ctl));
+    return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_BYTES + static_cast<int>(sizeof(Ctl));
 }
-static_assert(ST_MAX * K_MAX / TILE_M + SE_MAX < 65536, "m-tile numbers are 16 bits");
+static_assert(ST_MAX * K_MAX / TILE_FEW + SE_MAX < 65536, "m-tile numbers are 16 bits");
 static_assert(smem_bytes<128>() <= 232448 - 64 && smem_bytes<64>() <= 232448 - 64, "shared memory budget");
-// an MMA reads 128 activation rows: those past a 64-row region are bytes of
-// the next region (their sums are not used)
-static_assert((TILE_M - 64) * BLK <= Ring<64>::OUT_STAGES * OUT_STAGE, "the last stage's operand must end inside the block's memory");
-
 // ---------------------------------------------------------------- PTX --
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // Time for the bounded waits: SM cycles at the highest clock, so that a limit
@@ -203,15 +210,17 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (format code 0), fp32
-// accumulator, both K-major, M = 128, N = 256.
-constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE_N >> 3) << 17) |
-                           (static_cast<uint32_t>(TILE_M >> 4) << 24);
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+// accumulator, both K-major, M = 128, N = n (a multiple of 16).
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
+}
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // 32 consecutive fp32 columns of the warp's 32 TMEM lanes; the registers
@@ -262,6 +271,7 @@ __device__ __forceinline__ bool wait_bar(unsigned long long *b, unsigned parity,
 // column tiles, within one the m-tiles (CTAs that run together then share
 // weights in L2).  A slot without entries holds no m-tile: the search takes
 // the last slot whose first m-tile is at most t / nbt.
+template <int AR>
 __device__ Tile tile_at(int t, int phase, int nbt, const Ctl *ctl) {
     int lo = 0, hi = ctl->n_slots - 1;
     const int v = t / nbt;
@@ -278,13 +288,14 @@ __device__ Tile tile_at(int t, int phase, int nbt, const Ctl *ctl) {
     x.nb = r / mts;
     const int m = r - x.nb * mts;
     x.mt = ctl->mt[lo] + m;
-    x.p0 = ctl->off[lo] + m * TILE_M;
-    x.n = min(TILE_M, ctl->off[lo + 1] - x.p0);
+    x.p0 = ctl->off[lo] + m * AR;
+    x.n = min(AR, ctl->off[lo + 1] - x.p0);
     return x;
 }
 
 // The call's slots from the lists, checked before anything indexes with
 // them: inconsistent lists run as an empty call and are recorded.
+template <int AR>
 __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
     __shared__ int s_bad;
     const int most = min(a.E, a.B * a.k);
@@ -312,7 +323,7 @@ __device__ void build_slots(Ctl *ctl, const ProductArgs &a) {
         int run = 0;
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + threadIdx.x;
-            int v = i < n ? (ctl->off[i + 1] - ctl->off[i] + TILE_M - 1) / TILE_M : 0;
+            int v = i < n ? (ctl->off[i + 1] - ctl->off[i] + AR - 1) / AR : 0;
             const int mine = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -355,6 +366,7 @@ struct TileCursor {
 // Claims tiles ahead of the other roles (with the activation rows of their
 // entries), and publishes finished gate/up tiles: the fence before a
 // publication takes a microsecond that the epilogue does not wait for.
+template <int AR>
 __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
     const int lane = threadIdx.x & 31;
     const int nbt0 = column_tiles(a.phase[0]), t0 = ctl->m_tiles * nbt0;
@@ -374,8 +386,8 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
             Tile x;
             x.phase = TILE_END;
             x.n = x.ready = 0;
-            if (t < t0) x = tile_at(t, 0, nbt0, ctl);
-            else if (t < total) x = tile_at(t - t0, 1, nbt1, ctl);
+            if (t < t0) x = tile_at<AR>(t, 0, nbt0, ctl);
+            else if (t < total) x = tile_at<AR>(t - t0, 1, nbt1, ctl);
             int tok[4];
             if (x.phase != TILE_END) {
                 const bool by_pair = a.phase[x.phase].by_pair != 0;
@@ -595,15 +607,25 @@ __device__ void issue_role(unsigned char *ring, Ctl *ctl, const ProductArgs &a) 
         if (x.phase == TILE_END) return;
         const int kb = (a.phase[x.phase].K + BLK - 1) / BLK;
         for (int j = 0; j < kb; ++j, ++it) {
-            const int st = it % R::STAGES, buf = it & 1;
-            if (it >= 2 && !wait_bar(&ctl->part_free[buf], ((it >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP)) return;
+            const int st = it % R::STAGES, buf = it % R::BUFS;
+            if (it >= R::BUFS && !wait_bar(&ctl->part_free[buf], (it / R::BUFS - 1) & 1, ctl, a, DEV_TIMEOUT_DEP)) return;
             if (!wait_bar(&ctl->full[st], (it / R::STAGES) & 1, ctl, a, DEV_TIMEOUT_FULL)) return;
             tc_fence_after();
-            const uint64_t b = umma_desc(saddr(ring + st * R::STAGE));
+            const uint64_t w = umma_desc(saddr(ring + st * R::STAGE));
             const uint64_t v = umma_desc(saddr(ring + st * R::STAGE + W_STAGE));
+            const uint32_t d = tmem + buf * R::BUF_COLS;
+            if constexpr (R::FEW) {
+                const uint64_t w1 = umma_desc(saddr(ring + st * R::STAGE + W_STAGE / 2));
+                const uint32_t idesc = idesc_e4m3((x.n + 15) & ~15);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)  // 32 columns = 32 bytes each
-                umma_e4m3(tmem + buf * TILE_N, v + 2 * s, b + 2 * s, s > 0);
+                for (int s = 0; s < 4; ++s) {  // 32 columns = 32 bytes each
+                    umma_e4m3(d, w + 2 * s, v + 2 * s, idesc, s > 0);
+                    umma_e4m3(d + TILE_FEW, w1 + 2 * s, v + 2 * s, idesc, s > 0);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) umma_e4m3(d, v + 2 * s, w + 2 * s, idesc_e4m3(TILE_N), s > 0);
+            }
             umma_commit(saddr(&ctl->empty[st]));
             umma_commit(saddr(&ctl->part_full[buf]));
         }
@@ -685,13 +707,146 @@ __device__ __forceinline__ void store_out(unsigned char *stage, const float (&c)
     }
 }
 
-template <int AR>
-__device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
+// A finished tile of a two-phase call, for the warp that publishes: all
+// epilogue warps, after their stores.  False: given up.
+__device__ __forceinline__ bool hand_over(Ctl *ctl, const ProductArgs &a, unsigned n, int mt) {
+    const int slot = n & 1;
+    if (n >= 2 && !__all_sync(ALL, wait_bar(&ctl->pub_free[slot], ((n >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP))) return false;
+    if (threadIdx.x == 0) ctl->pub_mt[slot] = mt;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(&ctl->pub_full[slot]);
+    return true;
+}
+
+__device__ __forceinline__ int scale_exponent(float top) {
+    const unsigned tb = __float_as_uint(top);
+    const int e = tb == 0u ? 0 : static_cast<int>(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < -120 ? -120 : e;
+}
+// silu(g) u; the fast exp and division are good to a few units of fp32, and
+// h is about to be rounded to 4 bits
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// Few entries: thread (weight row, entry half) holds the row of both
+// matrices for up to 32 entries.
+__device__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
+    using R = Ring<TILE_FEW>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int m = quarter * 32 + lane;  // row of either matrix
+    bool dead = false;
+    unsigned it = 0, gu = 0, sg = 0;
+    TileCursor cur;
+    Tile x;
+    for (;;) {
+        dead = dead || !cur.next(ctl, a, x);
+        if (epi_any(dead)) return;  // together, so that none is left at a barrier
+        __syncwarp();
+        if (lane == 0) cur.release(ctl);
+        else ++cur.i;
+        if (x.phase == TILE_END) return;
+        const ProductPhase &ph = a.phase[x.phase];
+        const int kb = (ph.K + BLK - 1) / BLK;
+        const int wide = ((x.n + 15) & ~15) / 2;            // entries of a half
+        const int first = half * wide, n = min(wide, x.n - first);  // the warp's entries (n <= 0: none)
+        const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + first;
+        float c0[32], c1[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) c0[i] = c1[i] = 0.0f;
+        for (int j = 0; j < kb; ++j, ++it) {
+            const int buf = it % R::BUFS, sc = sg % SCALES;
+            bool ok = !dead;
+            if (j % SGROUP == 0) ok = ok && wait_bar(&ctl->scale_full[sc], (sg / SCALES) & 1, ctl, a, DEV_TIMEOUT_FULL);
+            ok = ok && wait_bar(&ctl->part_full[buf], (it / R::BUFS) & 1, ctl, a, DEV_TIMEOUT_FULL);
+            dead = !__all_sync(ALL, ok);
+            const bool last = j % SGROUP == SGROUP - 1 || j + 1 == kb;  // of the group
+            sg += last;
+            if (dead) continue;
+            tc_fence_after();
+            const float w0 = ctl->wscale[sc][0][j % SGROUP], w1 = ctl->wscale[sc][1][j % SGROUP];
+            const float *as = reinterpret_cast<const float *>(&ctl->scale[sc][first]) + j % SGROUP;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q * 8 < n) {
+                    float u[8], v[8];
+                    tmem_ld8(tbase + buf * R::BUF_COLS + q * 8, u);
+                    tmem_ld8(tbase + buf * R::BUF_COLS + TILE_FEW + q * 8, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float f = as[(q * 8 + i) * SGROUP];
+                        c0[q * 8 + i] = fmaf(u[i], f * w0, c0[q * 8 + i]);
+                        c1[q * 8 + i] = fmaf(v[i], f * w1, c1[q * 8 + i]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(&ctl->part_free[buf]);
+                if (last) bar_arrive(&ctl->scale_free[sc]);
+            }
+        }
+        if (ph.kind == PRODUCT_SWIGLU) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i < n) {  // the same for the whole warp
+                    c0[i] = swiglu(c0[i], c1[i]);
+                    const unsigned t = __reduce_max_sync(ALL, __float_as_uint(c0[i]) & 0x7fffffffu);
+                    if (lane == 0) ctl->top[quarter][first + i] = __uint_as_float(t);
+                }
+            }
+            epi_bar();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i < n) {
+                    const int c = first + i;
+                    const int e = scale_exponent(fmaxf(fmaxf(ctl->top[0][c], ctl->top[1][c]), fmaxf(ctl->top[2][c], ctl->top[3][c])));
+                    out_stage[c * BLK + m] =
+                        static_cast<unsigned char>(pack_e4m3(c0[i] * __int_as_float((127 - e) << 23), 0.f, 0.f, 0.f));
+                    if (m == 0 && !dead)
+                        ph.hs[static_cast<size_t>(x.p0 + c) * ph.hs_pitch + x.nb] = __int_as_float((127 + e) << 23);
+                }
+            }
+            epi_bar();
+            const int f0 = x.nb * BLK;
+            for (int i = threadIdx.x; i < x.n * 8 && !dead; i += 32 * EPI_WARPS) {
+                const int c = i >> 3, f = (i & 7) * 16;
+                if (f0 + f < ph.rows)
+                    *reinterpret_cast<uint4 *>(ph.hq + static_cast<size_t>(x.p0 + c) * ph.rows + f0 + f) =
+                        *reinterpret_cast<const uint4 *>(out_stage + c * BLK + f);
+            }
+            if (a.phases > 1 && !dead) dead = !hand_over(ctl, a, gu++, x.mt);
+        } else if (!dead) {
+            // a warp's lanes are neighbours in the output row: whole lines
+            const int r0 = x.nb * TILE_N + m;
+            const bool in0 = r0 < ph.rows, in1 = r0 + BLK < ph.rows;
+            const size_t at = static_cast<size_t>(x.p0 + first) * ph.rows + r0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i < n) {
+                    const size_t o = at + static_cast<size_t>(i) * ph.rows;
+                    if (ph.out_bf16) {
+                        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(ph.out);
+                        if (in0) y[o] = __float2bfloat16_rn(c0[i]);
+                        if (in1) y[o + BLK] = __float2bfloat16_rn(c1[i]);
+                    } else {
+                        float *y = static_cast<float *>(ph.out);
+                        if (in0) y[o] = c0[i];
+                        if (in1) y[o + BLK] = c1[i];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Many entries: thread (entry, column half).
+__device__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .., columns 64 half .. of each matrix
     const int row = quarter * 32 + lane;
     const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
-    unsigned char *stage = out_stage + (half * (AR / 32) + quarter) * OUT_STAGE;  // used by warps with rows
+    unsigned char *stage = out_stage + warp * OUT_STAGE;
     bool dead = false;
     unsigned it = 0, gu = 0, sg = 0;
     TileCursor cur;
@@ -760,9 +915,7 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
             if (live) {
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    // silu(g) u; the fast exp and division are good to a few
-                    // units of fp32, and h is about to be rounded to 4 bits
-                    c0[i] = __fdividef(c0[i], 1.0f + __expf(-c0[i])) * c1[i];
+                    c0[i] = swiglu(c0[i], c1[i]);
                     top = fmaxf(top, fabsf(c0[i]));
                 }
             }
@@ -771,9 +924,7 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
             epi_bar();
             if (live && !dead) {
                 top = fmaxf(ctl->top[0][row], ctl->top[1][row]);
-                const unsigned tb = __float_as_uint(top);
-                int e = tb == 0u ? 0 : static_cast<int>(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
-                e = e < -120 ? -120 : e;
+                const int e = scale_exponent(top);
                 const float inv = __int_as_float((127 - e) << 23);
                 uint4 o[4];
                 unsigned *w = reinterpret_cast<unsigned *>(o);
@@ -786,12 +937,7 @@ __device__ void epilogue_role(unsigned char *out_stage, Ctl *ctl, const ProductA
                 if (row < x.n && half == 0)
                     ph.hs[static_cast<size_t>(x.p0 + row) * ph.hs_pitch + x.nb] = __int_as_float((127 + e) << 23);
             }
-            const int slot = gu & 1;
-            if (gu >= 2 && !dead) dead = !__all_sync(ALL, wait_bar(&ctl->pub_free[slot], ((gu >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP));
-            ++gu;
-            if (threadIdx.x == 0) ctl->pub_mt[slot] = x.mt;
-            __syncwarp();
-            if (lane == 0 && !dead) bar_arrive(&ctl->pub_full[slot]);
+            if (!dead) dead = !hand_over(ctl, a, gu++, x.mt);
         } else if (live && !dead) {
             const int n0 = x.nb * TILE_N + half * 64;
             store_out(stage, c0, ph, row0, n0, rows_here, lane);
@@ -808,14 +954,14 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     unsigned char *ring =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *out_stage = ring + R::STAGES * R::STAGE;
-    Ctl *ctl = reinterpret_cast<Ctl *>(out_stage + R::OUT_STAGES * OUT_STAGE);
+    Ctl *ctl = reinterpret_cast<Ctl *>(out_stage + R::OUT_BYTES);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::STAGES; ++i) {
             bar_init(&ctl->full[i], 2);  // weights and rows
             bar_init(&ctl->empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R::BUFS; ++i) {
             bar_init(&ctl->part_full[i], 1);
             bar_init(&ctl->part_free[i], EPI_WARPS);
         }
@@ -838,13 +984,14 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == EPI_WARPS + 1) tmem_alloc(saddr(&ctl->tmem), 512);
     tc_fence_before();
-    build_slots(ctl, a);  // ends in a block barrier
+    build_slots<AR>(ctl, a);  // ends in a block barrier
     tc_fence_after();
     if (warp < EPI_WARPS) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
-        epilogue_role<AR>(out_stage, ctl, a);
+        if constexpr (!R::FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+        if constexpr (R::FEW) epilogue_few(out_stage, ctl, a);
+        else epilogue_many(out_stage, ctl, a);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+        if constexpr (!R::FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
         if (warp == EPI_WARPS) {
             if (elect_one()) ctl->fills[0] = weights_role<AR>(ring, ctl, maps, a);
         } else if (warp == EPI_WARPS + 1) {
@@ -860,7 +1007,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             if ((threadIdx.x & 31) == 0) ctl->fills[1] = n;
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            scheduler(ctl, a);
+            scheduler<AR>(ctl, a);
         }
         __syncwarp();
     }
@@ -912,8 +1059,14 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
 
 int product_box_rows() { return BOX_ROWS; }
 
+// Tiles of 64 entries up to FEW_ENTRIES entries an expert on average.
+int product_tile_entries(const moe_dims_t &d) {
+    const long long pairs = static_cast<long long>(d.B) * d.k, experts = d.E < pairs ? d.E : pairs;
+    return d.B <= TILE_FEW || pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
+}
+
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
-    return a.B <= 64 ? launch_ar<64>(maps, a, s) : launch_ar<128>(maps, a, s);
+    return a.tile_entries == TILE_FEW ? launch_ar<TILE_FEW>(maps, a, s) : launch_ar<TILE_MANY>(maps, a, s);
 }
 
 }  // namespace moe

@@ -49,6 +49,7 @@ struct ProductMaps {
     PhaseMaps phase[2];
 };
 int product_box_rows();
+int product_tile_entries(const moe_dims_t &d);  // list entries per tile
 bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
                        uint64_t E, uint64_t rows, uint64_t K);
 
@@ -70,6 +71,7 @@ struct ProductPhase {
 struct ProductArgs {
     ProductPhase phase[2];
     int phases;
+    int tile_entries;     // product_tile_entries
     int B, E, k;          // dims of the lists
     const int32_t *n_active, *active, *offsets, *tok;
     int32_t *done;        // two phases: gate/up tiles done per m-tile
