@@ -59,7 +59,11 @@ constexpr int OUT_STAGE = 32 * OUT_PITCH;
 constexpr int SGROUP = 4;         // column blocks whose scales are copied together (16 bytes a row)
 constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
-constexpr int FEW_ENTRIES = 48;   // an expert's entries, on average, up to which tiles are of 64
+constexpr int PUBS = 4;           // tiles claimed and not yet published, at most
+// Entries of an expert, on average, up to which tiles are of 64 (expert FFN,
+// d 2048, d_ff 1024, 64 experts: 8 entries 79 against 84 us with tiles of
+// 128, 16 entries 88 and 87.5, 32 entries 101 and 92).
+constexpr int FEW_ENTRIES = 16;
 constexpr int BOX_ROWS = 32;      // activation rows per copy where they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
@@ -87,7 +91,7 @@ struct Ctl {
     unsigned long long part_full[4], part_free[4];
     unsigned long long scale_full[SCALES], scale_free[SCALES];
     unsigned long long tile_full[TILES], tile_free[TILES];
-    unsigned long long pub_full[2], pub_free[2];
+    unsigned long long pub_full[PUBS];
     unsigned long long mma_done;
     volatile int abort_flag;
     int n_slots, m_tiles;
@@ -95,7 +99,9 @@ struct Ctl {
     uint32_t tmem;
     Tile tile[TILES];
     int rows[TILES][TILE_MANY];          // activation row of each entry of a claimed tile
-    int pub_mt[2];                    // m-tile of a finished gate/up tile
+    Tile own[EPI_WARPS];              // many entries: each epilogue warp's tile, out of its registers
+    unsigned handed[EPI_WARPS];       // and the gate/up tiles it has handed over
+    int pub_mt[PUBS];                    // m-tile of a finished gate/up tile
     float4 scale[SCALES][TILE_MANY];     // each row's scales of a group of column blocks
     float wscale[SCALES][2][SGROUP];  // and the two weight blocks'
     float top[4][TILE_MANY];          // largest |h|: [column half][entry], few entries: [quarter of the rows][entry]
@@ -248,6 +254,24 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  : "memory");
 }
 
+// eight columns from each of two places, waited for
+__device__ __forceinline__ void tmem_ld8x2(uint32_t t0, uint32_t t1, float (&u)[8], float (&v)[8]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t0), "r"(t1)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        u[i] = __uint_as_float(r[i]);
+        v[i] = __uint_as_float(r[8 + i]);
+    }
+}
+
 // Bounded wait on an mbarrier phase; false once the CTA has given up.
 __device__ __forceinline__ bool wait_slow(unsigned long long *b, unsigned parity, Ctl *ctl, const ProductArgs &a, int code) {
     const unsigned long long t0 = cycles();
@@ -378,7 +402,7 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
         bool idle = true;
         const int s = claimed % TILES;
         bool slot = false;
-        if (open) slot = __all_sync(ALL, claimed < TILES || bar_test(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
+        if (open && to_publish - published < PUBS) slot = __all_sync(ALL, claimed < TILES || bar_test(&ctl->tile_free[s], (claimed / TILES - 1) & 1));
         if (slot) {
             int t = 0;
             if (lane == 0) t = atomicAdd(a.next_tile, 1);
@@ -434,15 +458,14 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
             }
             idle = false;
         }
-        if (published < to_publish && __all_sync(ALL, bar_test(&ctl->pub_full[published & 1], (published >> 1) & 1))) {
+        if (published < to_publish && __all_sync(ALL, bar_test(&ctl->pub_full[published % PUBS], (published / PUBS) & 1))) {
             if (lane == 0) {
-                const int mt = ctl->pub_mt[published & 1];
+                const int mt = ctl->pub_mt[published % PUBS];
                 // h and its scales, written by the epilogue's threads, are in
                 // memory for the copies of any CTA before the tile counts
                 fence_async();
                 __threadfence();
                 add_release(a.done + mt);
-                bar_arrive(&ctl->pub_free[published & 1]);
             }
             __syncwarp();
             ++published;
@@ -707,15 +730,13 @@ __device__ __forceinline__ void store_out(unsigned char *stage, const float (&c)
     }
 }
 
-// A finished tile of a two-phase call, for the warp that publishes: all
-// epilogue warps, after their stores.  False: given up.
-__device__ __forceinline__ bool hand_over(Ctl *ctl, const ProductArgs &a, unsigned n, int mt) {
-    const int slot = n & 1;
-    if (n >= 2 && !__all_sync(ALL, wait_bar(&ctl->pub_free[slot], ((n >> 1) - 1) & 1, ctl, a, DEV_TIMEOUT_DEP))) return false;
-    if (threadIdx.x == 0) ctl->pub_mt[slot] = mt;
+// The n-th finished gate/up tile, for the warp that publishes: all epilogue
+// warps, after their stores.  (A slot comes round again only once the tile
+// that had it is published: no more are claimed before.)
+__device__ __forceinline__ void hand_over(Ctl *ctl, unsigned n, int mt) {
+    if (threadIdx.x == 0) ctl->pub_mt[n % PUBS] = mt;
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) bar_arrive(&ctl->pub_full[slot]);
-    return true;
+    if ((threadIdx.x & 31) == 0) bar_arrive(&ctl->pub_full[n % PUBS]);
 }
 
 __device__ __forceinline__ int scale_exponent(float top) {
@@ -729,7 +750,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g,
 
 // Few entries: thread (weight row, entry half) holds the row of both
 // matrices for up to 32 entries.
-__device__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
+__device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
     using R = Ring<TILE_FEW>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;
@@ -769,8 +790,7 @@ __device__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductAr
             for (int q = 0; q < 4; ++q) {
                 if (q * 8 < n) {
                     float u[8], v[8];
-                    tmem_ld8(tbase + buf * R::BUF_COLS + q * 8, u);
-                    tmem_ld8(tbase + buf * R::BUF_COLS + TILE_FEW + q * 8, v);
+                    tmem_ld8x2(tbase + buf * R::BUF_COLS + q * 8, tbase + buf * R::BUF_COLS + TILE_FEW + q * 8, u, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float f = as[(q * 8 + i) * SGROUP];
@@ -815,7 +835,7 @@ __device__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductAr
                     *reinterpret_cast<uint4 *>(ph.hq + static_cast<size_t>(x.p0 + c) * ph.rows + f0 + f) =
                         *reinterpret_cast<const uint4 *>(out_stage + c * BLK + f);
             }
-            if (a.phases > 1 && !dead) dead = !hand_over(ctl, a, gu++, x.mt);
+            if (a.phases > 1 && !dead) hand_over(ctl, gu++, x.mt);
         } else if (!dead) {
             // a warp's lanes are neighbours in the output row: whole lines
             const int r0 = x.nb * TILE_N + m;
@@ -841,14 +861,15 @@ __device__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductAr
 }
 
 // Many entries: thread (entry, column half).
-__device__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
+__device__ __forceinline__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .., columns 64 half .. of each matrix
     const int row = quarter * 32 + lane;
     const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
     unsigned char *stage = out_stage + warp * OUT_STAGE;
     bool dead = false;
-    unsigned it = 0, gu = 0, sg = 0;
+    unsigned it = 0, sg = 0;
+    if (lane == 0) ctl->handed[warp] = 0;
     TileCursor cur;
     Tile x;
     for (;;) {
@@ -858,9 +879,10 @@ __device__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductA
         if (lane == 0) cur.release(ctl);
         else ++cur.i;
         if (x.phase == TILE_END) return;
-        const ProductPhase &ph = a.phase[x.phase];
-        const int kb = (ph.K + BLK - 1) / BLK;
+        const int kb = (a.phase[x.phase].K + BLK - 1) / BLK;
         const bool live = quarter * 32 < x.n;  // the warp holds rows of the tile
+        if (lane == 0) ctl->own[warp] = x;
+        __syncwarp();
         float c0[64], c1[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) c0[i] = c1[i] = 0.0f;
@@ -908,6 +930,12 @@ __device__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductA
                 }
             }
         }
+        const volatile Tile *own = &ctl->own[warp];
+        x.phase = own->phase;
+        x.p0 = own->p0;
+        x.n = own->n;
+        x.nb = own->nb;
+        const ProductPhase &ph = a.phase[x.phase];
         const int rows_here = min(32, x.n - quarter * 32);
         const size_t row0 = static_cast<size_t>(x.p0 + quarter * 32);
         if (ph.kind == PRODUCT_SWIGLU) {
@@ -937,7 +965,12 @@ __device__ void epilogue_many(unsigned char *out_stage, Ctl *ctl, const ProductA
                 if (row < x.n && half == 0)
                     ph.hs[static_cast<size_t>(x.p0 + row) * ph.hs_pitch + x.nb] = __int_as_float((127 + e) << 23);
             }
-            if (!dead) dead = !hand_over(ctl, a, gu++, x.mt);
+            if (!dead) {
+                const unsigned n = const_cast<volatile unsigned *>(ctl->handed)[warp];
+                __syncwarp();
+                if (lane == 0) ctl->handed[warp] = n + 1;
+                hand_over(ctl, n, own->mt);
+            }
         } else if (live && !dead) {
             const int n0 = x.nb * TILE_N + half * 64;
             store_out(stage, c0, ph, row0, n0, rows_here, lane);
@@ -973,10 +1006,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             bar_init(&ctl->tile_full[i], 1);
             bar_init(&ctl->tile_free[i], EPI_WARPS + 3);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(&ctl->pub_full[i], EPI_WARPS);
-            bar_init(&ctl->pub_free[i], 1);
-        }
+        for (int i = 0; i < PUBS; ++i) bar_init(&ctl->pub_full[i], EPI_WARPS);
         bar_init(&ctl->mma_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ctl->abort_flag = 0;
@@ -1062,7 +1092,7 @@ int product_box_rows() { return BOX_ROWS; }
 // Tiles of 64 entries up to FEW_ENTRIES entries an expert on average.
 int product_tile_entries(const moe_dims_t &d) {
     const long long pairs = static_cast<long long>(d.B) * d.k, experts = d.E < pairs ? d.E : pairs;
-    return d.B <= TILE_FEW || pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
+    return pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
 }
 
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {

@@ -18,6 +18,8 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
+// Rows from which a warp takes 2048 (bf16) or 1024 (fp32) columns instead of
+// 512 (4096 x 2048 bf16: 4.65 against 4.99 us).
 constexpr long long WIDE_ROWS = 2048;
 
 // Exponent e of the scale 2^e for a block whose largest magnitude is top
