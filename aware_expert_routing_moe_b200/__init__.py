@@ -348,6 +348,20 @@ def _stream_of(stream, t):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _buf(t, nbytes: int):
+    """Pointer of a contiguous tensor of at least nbytes bytes (the library
+    sees no sizes)."""
+    if isinstance(t, torch.Tensor) and t.nbytes < nbytes:
+        raise ValueError(f"tensor of {t.nbytes} bytes where the call's sizes need {nbytes}")
+    return _ptr(t)
+
+
+def _list_bufs(l: dict, B: int, E: int, k: int) -> Lists:
+    pairs = 4 * B * k
+    return Lists(_buf(l["n_active"], 4), _buf(l["active"], 4 * E), _buf(l["offsets"], 4 * E + 4), _buf(l["tok"], pairs),
+                 _buf(l["w"], pairs))
+
+
 def _dtype(t) -> int:
     code = _DTYPES.get(t if isinstance(t, torch.dtype) else t.dtype)
     if code is None:
@@ -398,9 +412,9 @@ def moe_route_scored(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, 
         ws = new_route_workspace(B, E, k, logits.device)
     sel, w = out
     st = (_lib or load_library()).moe_route_scored(
-        _ptr(logits), _ptr(bias), _dims(B, 0, E, k, 0),
-        _scoring(score, groups, top_groups, group_best, int(renorm), float(scale)), _ptr(sel), _ptr(w), _lists(lists),
-        _ptr(ws), _bytes(ws), _stream_of(stream, logits))
+        _ptr(logits), None if bias is None else _buf(bias, 4 * E), _dims(B, 0, E, k, 0),
+        _scoring(score, groups, top_groups, group_best, int(renorm), float(scale)), _buf(sel, 4 * B * k),
+        _buf(w, 4 * B * k), _list_bufs(lists, B, E, k), _ptr(ws), _bytes(ws), _stream_of(stream, logits))
     _check(st, "moe_route_scored")
     return sel, w, lists
 
@@ -414,11 +428,12 @@ def moe_quantize_blocks(x, block_rows: int = 1, q=None, scale=None, stream=None)
     batch = x.numel() // (rows * cols) if rows * cols else 0
     if q is None:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    rb, cb = rows if block_rows == 1 else -(-rows // 128), -(-cols // 128)
     if scale is None:
-        rb = rows if block_rows == 1 else -(-rows // 128)
-        scale = torch.empty((*shape[:-2], rb, -(-cols // 128)), dtype=torch.float32, device=x.device)
-    st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows, _ptr(q),
-                                                      _ptr(scale), _stream_of(stream, x))
+        scale = torch.empty((*shape[:-2], rb, cb), dtype=torch.float32, device=x.device)
+    st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows,
+                                                      _buf(q, batch * rows * cols), _buf(scale, 4 * batch * rb * cb),
+                                                      _stream_of(stream, x))
     _check(st, "moe_quantize_blocks")
     return q, scale
 
@@ -434,9 +449,11 @@ def moe_expert_gemm_blocks(q, scale, W, Wscale, lists: dict, k: int, ws=None, y=
         ws = new_gemm_workspace(q.device)
     if y is None:
         y = torch.empty(B * k, F, dtype=y_dtype, device=q.device)
+    cb, rb = -(-d // 128), -(-F // 128)
     st = (_lib or load_library()).moe_expert_gemm_blocks(
-        _ptr(q), _ptr(scale), _ptr(W), _ptr(Wscale), _dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws),
-        _bytes(ws), _stream_of(stream, q))
+        _ptr(q), _buf(scale, 4 * B * cb), _buf(W, E * F * d), _buf(Wscale, 4 * E * rb * cb), _dims(B, d, E, k, F),
+        _list_bufs(lists, B, E, k), _buf(y, B * k * F * y.element_size()), _dtype(y), _ptr(ws), _bytes(ws),
+        _stream_of(stream, q))
     _check(st, "moe_expert_gemm_blocks")
     return y
 
@@ -451,9 +468,12 @@ def moe_expert_ffn_blocks(x, Wgate, Sgate, Wup, Sup, Wdown, Sdown, lists: dict, 
         ws = new_blocks_workspace(B, d, E, k, F, x.device)
     if y is None:
         y = torch.empty(B, d, dtype=y_dtype or x.dtype, device=x.device)
+    n, ns = E * F * d, 4 * E * -(-F // 128) * -(-d // 128)
     st = (_lib or load_library()).moe_expert_ffn_blocks(
-        _ptr(x), _dtype(x), BlockWeights(_ptr(Wgate), _ptr(Sgate), _ptr(Wup), _ptr(Sup), _ptr(Wdown), _ptr(Sdown)),
-        _dims(B, d, E, k, F), _lists(lists), _ptr(y), _dtype(y), _ptr(ws), _bytes(ws), _stream_of(stream, x))
+        _ptr(x), _dtype(x),
+        BlockWeights(_buf(Wgate, n), _buf(Sgate, ns), _buf(Wup, n), _buf(Sup, ns), _buf(Wdown, n), _buf(Sdown, ns)),
+        _dims(B, d, E, k, F), _list_bufs(lists, B, E, k), _buf(y, B * d * y.element_size()), _dtype(y), _ptr(ws),
+        _bytes(ws), _stream_of(stream, x))
     _check(st, "moe_expert_ffn_blocks")
     return y
 

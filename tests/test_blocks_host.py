@@ -156,6 +156,28 @@ def test_binding_refuses_other_types_and_strides(lib):
                                 scale=torch.zeros(4, 1), stream=0)
 
 
+def test_binding_refuses_short_buffers_and_host_tensors(lib):
+    z = lambda *n, t=torch.uint8: torch.zeros(*n, dtype=t)
+    f = lambda *n: torch.zeros(*n)
+    lists = moe.alloc_lists(4, 8, 2, device="cpu")
+    ok = dict(x=f(4, 256), Wgate=z(8, 128, 256), Sgate=f(8, 1, 2), Wup=z(8, 128, 256), Sup=f(8, 1, 2),
+              Wdown=z(8, 256, 128), Sdown=f(8, 2, 1), lists=lists, k=2, ws=z(1 << 20), y=f(4, 256), stream=0)
+    for name, short in (("Sgate", f(8, 1, 1)), ("Wup", z(8, 127, 256)), ("Wdown", z(8, 255, 128)), ("Sdown", f(15)),
+                        ("y", f(3, 256)), ("lists", dict(lists, tok=lists["tok"][:7])),
+                        ("lists", dict(lists, offsets=lists["offsets"][:8]))):
+        with pytest.raises(ValueError):
+            moe.moe_expert_ffn_blocks(**dict(ok, **{name: short}))
+    with pytest.raises(ValueError):
+        moe.moe_expert_gemm_blocks(z(4, 256), f(4, 1), z(8, 128, 256), f(8, 1, 2), lists, 2, ws=z(4096), y=f(8, 128), stream=0)
+    with pytest.raises(ValueError):
+        moe.moe_quantize_blocks(f(4, 256), q=z(4, 255), scale=f(4, 2), stream=0)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(f(4, 8), 2, bias=f(7), out=(z(4, 2, t=torch.int32), f(4, 2)), lists=lists, ws=z(4096), stream=0)
+    # without a stream of the caller's, tensors have to be on the current device
+    with pytest.raises(ValueError):
+        moe.moe_quantize_blocks(f(4, 256))
+
+
 # ------------------------------------------- the restatements themselves --
 def test_e4m3_restatement():
     b = np.arange(256, dtype=np.uint8)

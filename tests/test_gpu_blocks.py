@@ -270,3 +270,141 @@ def test_bad_lists_are_reported(field, value):
     y = moe.moe_expert_ffn_blocks(x, *args, dev, 3, ws=ws)
     assert moe.moe_check_error(ws) == 0
     _check_ffn(y, x, L, vals)
+
+
+# ------------------------------------------------- workspaces and waits --
+@pytest.mark.parametrize("B,E", [(20, 6), (150, 4)])  # tiles of 64 and of 128 entries
+def test_an_expired_wait_is_reported_and_the_device_stays_usable(B, E):
+    d, k, F = 512, 3, 256
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+    ws, gws = moe.new_blocks_workspace(B, d, E, k, F), moe.new_gemm_workspace()
+    q, s = moe.moe_quantize_blocks(x)
+    torch.cuda.synchronize()
+    try:
+        moe.moe_set_wait_limit_ns(1)
+        moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws)
+        assert moe.moe_check_error(ws) == 6
+        moe.moe_expert_gemm_blocks(q, s, args[0], args[1], dev, k, ws=gws)
+        assert moe.moe_check_error(gws) == 6
+    finally:
+        moe.moe_set_wait_limit_ns(0)
+    ws.zero_()
+    gws.zero_()
+    y = moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, vals)
+
+
+def test_one_workspace_for_calls_of_other_sizes():
+    cases = [_ffn_setup(B, d, E, k, F, BF16, seed=B) + (k,) for B, d, E, k, F in
+             [(70, 512, 8, 3, 256), (3, 128, 4, 2, 384), (200, 256, 2, 2, 128), (1, 1024, 8, 8, 256)]]
+    ws = torch.zeros(max(moe.new_blocks_workspace(c[2].shape[0], c[2].shape[1], c[3][0].shape[0], c[5],
+                                                  c[3][0].shape[1]).numel() for c in cases), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for L, dev, x, args, vals, k in cases:
+            y = moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws)
+            _check_ffn(y, x, L, vals)
+    assert moe.moe_check_error(ws) == 0
+
+
+def test_two_streams_at_once():
+    a, b = _ffn_setup(90, 512, 4, 2, 512, BF16, seed=3), _ffn_setup(12, 512, 16, 4, 512, BF16, seed=4)
+    k = (2, 4)
+    want = [moe.moe_expert_ffn_blocks(c[2], *c[3], c[1], n) for c, n in zip((a, b), k)]
+    ws = [moe.new_blocks_workspace(90, 512, 4, 2, 512), moe.new_blocks_workspace(12, 512, 16, 4, 512)]
+    ys = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, c in enumerate((a, b)):
+            moe.moe_expert_ffn_blocks(c[2], *c[3], c[1], k[i], ws=ws[i], y=ys[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i, c in enumerate((a, b)):
+        assert moe.moe_check_error(ws[i]) == 0
+        assert torch.equal(ys[i], want[i])
+    _check_ffn(want[0], a[2], a[0], a[4])
+    _check_ffn(want[1], b[2], b[0], b[4])
+
+
+def test_two_captured_graphs_take_turns_in_one_workspace():
+    a, b = _ffn_setup(30, 256, 4, 2, 256, BF16, seed=5), _ffn_setup(150, 256, 4, 2, 256, BF16, seed=6)
+    ws = moe.new_blocks_workspace(150, 256, 4, 2, 256)
+    ys = [torch.zeros(30, 256, dtype=BF16, device="cuda"), torch.zeros(150, 256, dtype=BF16, device="cuda")]
+    graphs = []
+    for c, y in zip((a, b), ys):
+        moe.moe_expert_ffn_blocks(c[2], *c[3], c[1], 2, ws=ws, y=y)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_expert_ffn_blocks(c[2], *c[3], c[1], 2, ws=ws, y=y)
+        graphs.append(g)
+    for y in ys:
+        y.zero_()
+    for i in (0, 1, 0, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(ys[0], a[2], a[0], a[4])
+    _check_ffn(ys[1], b[2], b[0], b[4])
+
+
+# ------------------------------------------------------- long and chained --
+def test_quantize_past_two_to_the_31():
+    rows, cols = 33000, 65536
+    x = torch.zeros(rows, cols, dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for r in (0, 16384, 32767, 32768, 32999):
+        x[r] = torch.randn(cols, device="cuda", generator=g).to(BF16)
+    q, s = moe.moe_quantize_blocks(x)
+    for r in (0, 1, 16384, 32767, 32768, 32998, 32999):
+        rq, rs = bc.quantize(x[r:r + 1].double().cpu().numpy())
+        assert np.array_equal(_values(q[r:r + 1]), rq) and np.array_equal(s[r:r + 1].double().cpu().numpy(), rs)
+
+
+def test_ffn_past_two_to_the_31():
+    # B * k * d = 2.2e9 values of dispatched rows and of down products
+    B, d, E, k, F = 17000, 16384, 8, 8, 16
+    rng = np.random.default_rng(9)
+    sel = np.tile(np.arange(8, dtype=np.int32), (B, 1))
+    w = (rng.random((B, k)) + 0.1).astype(np.float32)
+    tok = np.tile(np.arange(B, dtype=np.int32), E)
+    dev = {"n_active": _cuda(np.array([E, 0, 0, 0], np.int32)), "active": _cuda(np.arange(E, dtype=np.int32)),
+           "offsets": _cuda((np.arange(E + 1) * B).astype(np.int32)), "tok": _cuda(tok), "w": _cuda(w.T.reshape(-1))}
+    x = torch.randn(B, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(BF16)
+    mats = [_weights(rng, E, F, d), _weights(rng, E, F, d), _weights(rng, E, d, F)]
+    ws = moe.new_blocks_workspace(B, d, E, k, F)
+    y = moe.moe_expert_ffn_blocks(x, *[t for m in mats for t in m[:2]], dev, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    at = np.array([0, 1, 8191, 16383, 16998, 16999])
+    L = bc.lists_of(sel[at], w[at], E)
+    _check_ffn(y[torch.from_numpy(at).cuda()], x[torch.from_numpy(at).cuda()], L, [m[2] for m in mats])
+
+
+@pytest.mark.parametrize("B", [1, 37, 200])
+def test_router_scored_router_and_both_expert_ffns(B):
+    # as a layer uses them: logits, choice and lists, then the experts in 8
+    # bits and, from the same lists, in bf16
+    d, E, k, F = 512, 32, 4, 256
+    rng = np.random.default_rng([11, B])
+    x = torch.from_numpy(rng.standard_normal((B, d)).astype(np.float32)).cuda()
+    Wg = torch.from_numpy((rng.standard_normal((E, d)) * 0.05).astype(np.float32)).cuda()
+    beta = torch.from_numpy((rng.standard_normal(E) * 0.05).astype(np.float32)).cuda()
+    logits, _, _, _ = moe.moe_route(x, Wg, None, k)
+    sel, w, lists = moe.moe_route_scored(logits, k, moe.MOE_SCORE_SIGMOID, bias=beta, groups=4, top_groups=2,
+                                         group_best=2, scale=2.5)
+    rsel, rw = bc.route(logits.cpu().numpy(), k, True, beta.cpu().numpy(), 4, 2, 2, True, 2.5)
+    assert np.array_equal(sel.cpu().numpy(), rsel)
+    L = bc.lists_of(rsel, w.cpu().numpy(), E)
+    W = [torch.from_numpy((rng.standard_normal((E, r, c)) * 0.05).astype(np.float32)).cuda()
+         for r, c in ((F, d), (F, d), (d, F))]
+    quant = [moe.moe_quantize_blocks(m, 128) for m in W]
+    vals = [np.stack([v * bc.spread(t, *v.shape, 128) for v, t in zip(_values(q), s.double().cpu().numpy())])
+            for q, s in quant]
+    ws = moe.new_blocks_workspace(B, d, E, k, F)
+    y = moe.moe_expert_ffn_blocks(x, *[t for m in quant for t in m], lists, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, vals)
+    yb = moe.moe_expert_ffn(x, *[m.to(BF16).view(torch.int16) for m in W], lists, k, moe.new_workspace(B, d, E, k, F))
+    # e4m3 keeps three bits: x, the weights and h are each off by 2^-4 of
+    # themselves at most, and the errors are independent
+    assert float((y - yb).norm() / yb.norm()) < 4 * 2.0 ** -4
