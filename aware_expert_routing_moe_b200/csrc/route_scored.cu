@@ -260,17 +260,26 @@ __device__ __noinline__ int by_value(const RouteArgs &a, double (&c)[NI], double
 
 __device__ __forceinline__ float clean_logit(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
 
+template <int NI>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, int b, int last, float (&l)[NI]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        l[i] = b < last && lane + 32 * i < a.E ? __ldg(a.logits + static_cast<size_t>(b) * a.E + lane + 32 * i) : -INFINITY;
+}
+
 // A token's choice and weights by one warp.
 template <int NI>
 __device__ __forceinline__ void choose(const RouteArgs &a, int b, const int (&group)[NI], const float (&bias)[NI],
-                                       double unit, unsigned *s_hist, double *row, int *s_sel, float *s_w) {
+                                       double unit, const float (&raw)[NI], unsigned *s_hist, double *row, int *s_sel,
+                                       float *s_w) {
     const int lane = threadIdx.x & 31;
     const bool sig = a.rule.score == MOE_SCORE_SIGMOID;
     const float *logits = a.logits + static_cast<size_t>(b) * a.E;
     Token<NI> t;
     float l[NI], top = -INFINITY, low = INFINITY;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) l[i] = lane + 32 * i < a.E ? clean_logit(__ldg(logits + lane + 32 * i)) : -INFINITY;
+    for (int i = 0; i < NI; ++i) l[i] = clean_logit(raw[i]);
     // with a bias, or groups valued by two experts, the values rank
     const bool may_logit = a.bias == nullptr && (a.rule.groups == 1 || a.rule.group_best == 1);
     if (may_logit || !sig) {
@@ -472,13 +481,14 @@ __global__ void __launch_bounds__(THREADS, NI <= 8 ? 2 : 1) route_choose_kernel(
     double *s_row = reinterpret_cast<double *>(smem);  // [warp][E + groups], groups only
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     s_hist[threadIdx.x] = 0;
-    const int per = a.E / a.rule.groups;
+    const float inv_per = static_cast<float>(a.rule.groups) / static_cast<float>(a.E);
     int group[NI];
     float bias[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = lane + 32 * i;
-        group[i] = a.rule.groups > 1 ? min(e, a.E - 1) / per : 0;
+        // e / per for small integers: (e + 1/2) / per is never near one
+        group[i] = a.rule.groups > 1 ? __float2int_rz((static_cast<float>(min(e, a.E - 1)) + 0.5f) * inv_per) : 0;
         bias[i] = a.bias != nullptr && e < a.E ? __ldg(a.bias + e) : 0.0f;
     }
     // images: scores are at most 1, so values are below 1 + the largest bias
@@ -490,8 +500,15 @@ __global__ void __launch_bounds__(THREADS, NI <= 8 ? 2 : 1) route_choose_kernel(
     const double unit = __hiloint2double((1023 + 26 - ex) << 20, 0);
     __syncthreads();
     const int first = blockIdx.x * a.run, last = min(first + a.run, a.B);
-    for (int b = first + warp; b < last; b += WARPS)
-        choose<NI>(a, b, group, bias, unit, s_hist, s_row + static_cast<size_t>(warp) * (a.E + a.rule.groups), sh.sel, sh.w);
+    // the next token's logits are on their way while a token is done
+    float raw[NI], next[NI];
+    load_logits<NI>(a, first + warp, last, next);
+    for (int b = first + warp; b < last; b += WARPS) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) raw[i] = next[i];
+        load_logits<NI>(a, b + WARPS, last, next);
+        choose<NI>(a, b, group, bias, unit, raw, s_hist, s_row + static_cast<size_t>(warp) * (a.E + a.rule.groups), sh.sel, sh.w);
+    }
     __syncthreads();
     if (!a.one_launch) {
         const int pitch = hist_pitch(a.E);
