@@ -603,7 +603,7 @@ moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const 
     if (st != MOE_OK) return st;
     ProductMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (!encode_phase_maps(&maps.phase[0], q, dims.B, product_box_rows(), W, W, dims.E, dims.d_ff, dims.d))
+    if (!encode_phase_maps(&maps.phase[0], q, dims.B, product_box_rows(dims), W, W, dims.E, dims.d_ff, dims.d))
         return MOE_ERR_CUDA;
     ProductArgs a = product_args(dims, lists, ws);
     a.phases = 1;
@@ -644,7 +644,7 @@ moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weig
     int32_t *counts = seg<int32_t>(ws, L.counts), *inv = seg<int32_t>(ws, L.inv);
     const int pairs = dims.B * dims.k;
     const bool dispatch = dims.B > DISPATCH_MIN;
-    const int rows = dispatch ? pairs : dims.B, box = product_box_rows();
+    const int rows = dispatch ? pairs : dims.B, box = product_box_rows(dims);
     ProductMaps maps;
     if (!encode_phase_maps(&maps.phase[0], xq, rows, box, w.Wgate, w.Wup, dims.E, dims.d_ff, dims.d) ||
         !encode_phase_maps(&maps.phase[1], hq, pairs, box, w.Wdown, w.Wdown, dims.E, dims.d, dims.d_ff))

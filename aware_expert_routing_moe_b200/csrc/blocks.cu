@@ -44,7 +44,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
-constexpr int TILE_MANY = 128, TILE_FEW = 64;  // list entries per tile
+constexpr int TILE_MANY = 128, TILE_FEW = 64, TILE_TINY = 16;  // list entries per tile
 constexpr int TILE_N = 256;       // weight rows per tile (128 + 128 for gate/up)
 constexpr int W_STAGE = TILE_N * BLK;  // weight bytes of a stage: 256 rows x 128 columns
 constexpr int EPI_WARPS = 8;
@@ -68,14 +68,15 @@ constexpr int BOX_ROWS = 32;      // activation rows per copy where they are con
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
 // A kernel for tiles of AR entries: AR activation rows per stage; with few
-// entries a fifth stage fits, and four TMEM buffers.
+// entries a fifth or sixth stage fits, and four TMEM buffers.
 template <int AR>
 struct Ring {
-    static constexpr bool FEW = AR == TILE_FEW;
+    static constexpr bool FEW = AR <= TILE_FEW;
     static constexpr int A_STAGE = AR * BLK;
     static constexpr int STAGE = W_STAGE + A_STAGE;
-    static constexpr int STAGES = FEW ? 5 : 4;
+    static constexpr int STAGES = AR == TILE_TINY ? 6 : FEW ? 5 : 4;
     static constexpr int OUT_BYTES = FEW ? AR * BLK : EPI_WARPS * OUT_STAGE;  // h of a tile, or a piece a warp
+    static constexpr int BOX = AR < BOX_ROWS ? AR : BOX_ROWS;  // rows per copy
     static constexpr int BUFS = FEW ? 4 : 2;          // TMEM buffers
     static constexpr int BUF_COLS = 512 / BUFS;       // two blocks of 64 entries, or 256 weight rows
 };
@@ -87,7 +88,7 @@ struct Tile {
 };
 
 struct Ctl {
-    unsigned long long full[5], empty[5];
+    unsigned long long full[6], empty[6];
     unsigned long long part_full[4], part_free[4];
     unsigned long long scale_full[SCALES], scale_free[SCALES];
     unsigned long long tile_full[TILES], tile_free[TILES];
@@ -113,7 +114,9 @@ constexpr int smem_bytes() {
     return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_BYTES + static_cast<int>(sizeof(Ctl));
 }
 static_assert(ST_MAX * K_MAX / TILE_FEW + SE_MAX < 65536, "m-tile numbers are 16 bits");
-static_assert(smem_bytes<128>() <= 232448 - 64 && smem_bytes<64>() <= 232448 - 64, "shared memory budget");
+static_assert(smem_bytes<TILE_MANY>() <= 232448 - 64 && smem_bytes<TILE_FEW>() <= 232448 - 64 &&
+                  smem_bytes<TILE_TINY>() <= 232448 - 64,
+              "shared memory budget");
 // ---------------------------------------------------------------- PTX --
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // Time for the bounded waits: SM cycles at the highest clock, so that a limit
@@ -573,14 +576,14 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
         const int nb = ph.kind == PRODUCT_SWIGLU ? x.nb : min(2 * x.nb + (lane >> 2), rb - 1);
         const float *wsrc = (lane < 4 ? ph.bs0 : ph.bs1) + (static_cast<size_t>(x.e) * rb + nb) * kb;
         const bool wide = (ph.as_pitch & 3) == 0;
-        // consecutive rows in boxes of BOX_ROWS, scattered ones four at a time
+        // consecutive rows in boxes, scattered ones four at a time
         const int first = __shfl_sync(ALL, rows[0], 0);
         bool run = true;
 #pragma unroll
         for (int q = 0; q < 4; ++q) run = run && rows[q] == first + min(lane * 4 + q, x.n - 1);
         const bool box = __all_sync(ALL, run);
-        const int copies = box ? (x.n + BOX_ROWS - 1) / BOX_ROWS : (x.n + 3) >> 2;
-        const unsigned copy_bytes = box ? BOX_ROWS * BLK : 4 * BLK, bytes = copies * copy_bytes;
+        const int copies = box ? (x.n + R::BOX - 1) / R::BOX : (x.n + 3) >> 2;
+        const unsigned copy_bytes = box ? R::BOX * BLK : 4 * BLK, bytes = copies * copy_bytes;
         const CUtensorMap *m = box ? &maps.phase[x.phase].ab : &maps.phase[x.phase].a;
         for (int j = 0; j < kb; ++j) {
             if (j % SGROUP == 0) {
@@ -606,7 +609,7 @@ __device__ unsigned rows_role(unsigned char *ring, Ctl *ctl, const ProductMaps &
             __syncwarp();
             if (lane < copies) {
                 unsigned char *d = ring + st * R::STAGE + W_STAGE + lane * copy_bytes;
-                if (box) load_rows(d, m, j * BLK, first + lane * BOX_ROWS, full);
+                if (box) load_rows(d, m, j * BLK, first + lane * R::BOX, full);
                 else load_rows4(d, m, j * BLK, rows, full);
             }
             ++it;
@@ -749,9 +752,11 @@ __device__ __forceinline__ int scale_exponent(float top) {
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // Few entries: thread (weight row, entry half) holds the row of both
-// matrices for up to 32 entries.
+// matrices for up to AR / 2 entries.
+template <int AR>
 __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
-    using R = Ring<TILE_FEW>;
+    using R = Ring<AR>;
+    constexpr int HALF = AR / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;
     const int m = quarter * 32 + lane;  // row of either matrix
@@ -771,9 +776,9 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
         const int wide = ((x.n + 15) & ~15) / 2;            // entries of a half
         const int first = half * wide, n = min(wide, x.n - first);  // the warp's entries (n <= 0: none)
         const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + first;
-        float c0[32], c1[32];
+        float c0[HALF], c1[HALF];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) c0[i] = c1[i] = 0.0f;
+        for (int i = 0; i < HALF; ++i) c0[i] = c1[i] = 0.0f;
         for (int j = 0; j < kb; ++j, ++it) {
             const int buf = it % R::BUFS, sc = sg % SCALES;
             bool ok = !dead;
@@ -787,7 +792,7 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
             const float w0 = ctl->wscale[sc][0][j % SGROUP], w1 = ctl->wscale[sc][1][j % SGROUP];
             const float *as = reinterpret_cast<const float *>(&ctl->scale[sc][first]) + j % SGROUP;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < HALF / 8; ++q) {
                 if (q * 8 < n) {
                     float u[8], v[8];
                     tmem_ld8x2(tbase + buf * R::BUF_COLS + q * 8, tbase + buf * R::BUF_COLS + TILE_FEW + q * 8, u, v);
@@ -808,7 +813,7 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
         }
         if (ph.kind == PRODUCT_SWIGLU) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < HALF; ++i) {
                 if (i < n) {  // the same for the whole warp
                     c0[i] = swiglu(c0[i], c1[i]);
                     const unsigned t = __reduce_max_sync(ALL, __float_as_uint(c0[i]) & 0x7fffffffu);
@@ -817,7 +822,7 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
             }
             epi_bar();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < HALF; ++i) {
                 if (i < n) {
                     const int c = first + i;
                     const int e = scale_exponent(fmaxf(fmaxf(ctl->top[0][c], ctl->top[1][c]), fmaxf(ctl->top[2][c], ctl->top[3][c])));
@@ -842,7 +847,7 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
             const bool in0 = r0 < ph.rows, in1 = r0 + BLK < ph.rows;
             const size_t at = static_cast<size_t>(x.p0 + first) * ph.rows + r0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < HALF; ++i) {
                 if (i < n) {
                     const size_t o = at + static_cast<size_t>(i) * ph.rows;
                     if (ph.out_bf16) {
@@ -1018,7 +1023,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     tc_fence_after();
     if (warp < EPI_WARPS) {
         if constexpr (!R::FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
-        if constexpr (R::FEW) epilogue_few(out_stage, ctl, a);
+        if constexpr (R::FEW) epilogue_few<AR>(out_stage, ctl, a);
         else epilogue_many(out_stage, ctl, a);
     } else {
         if constexpr (!R::FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
@@ -1087,16 +1092,22 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
 
 }  // namespace
 
-int product_box_rows() { return BOX_ROWS; }
-
-// Tiles of 64 entries up to FEW_ENTRIES entries an expert on average.
+// Tiles of 16 entries where no expert can have more, of 64 up to FEW_ENTRIES
+// an expert on average, else of 128.
 int product_tile_entries(const moe_dims_t &d) {
     const long long pairs = static_cast<long long>(d.B) * d.k, experts = d.E < pairs ? d.E : pairs;
-    return pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
+    return d.B <= TILE_TINY ? TILE_TINY : pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
+}
+
+int product_box_rows(const moe_dims_t &d) {
+    const int n = product_tile_entries(d);
+    return n < BOX_ROWS ? n : BOX_ROWS;
 }
 
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
-    return a.tile_entries == TILE_FEW ? launch_ar<TILE_FEW>(maps, a, s) : launch_ar<TILE_MANY>(maps, a, s);
+    return a.tile_entries == TILE_TINY  ? launch_ar<TILE_TINY>(maps, a, s)
+           : a.tile_entries == TILE_FEW ? launch_ar<TILE_FEW>(maps, a, s)
+                                        : launch_ar<TILE_MANY>(maps, a, s);
 }
 
 }  // namespace moe

@@ -48,7 +48,7 @@ struct PhaseMaps {
 struct ProductMaps {
     PhaseMaps phase[2];
 };
-int product_box_rows();
+int product_box_rows(const moe_dims_t &d);
 int product_tile_entries(const moe_dims_t &d);  // list entries per tile
 bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
                        uint64_t E, uint64_t rows, uint64_t K);
