@@ -312,7 +312,7 @@ BlocksWs blocks_ws(const moe_dims_t &d) {
     BlocksWs w;
     const size_t B = d.B, E = d.E, k = d.k, D = d.d, F = d.d_ff, P = B * k;
     size_t o = MOE_GEMM_WORKSPACE_BYTES;
-    const size_t rows = d.B > DISPATCH_MIN ? P : B;  // quantised activation rows
+    const size_t rows = product_dispatch(d) ? P : B;  // quantised activation rows
     w.xq = o;  o += round_up(rows * D);
     w.xs = o;  o += round_up(rows * scale_pitch(d.d) * 4);
     w.hq = o;  o += round_up(P * F);
@@ -643,7 +643,7 @@ moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weig
     float *xs = seg<float>(ws, L.xs), *hs = seg<float>(ws, L.hs), *yp = seg<float>(ws, L.yp);
     int32_t *counts = seg<int32_t>(ws, L.counts), *inv = seg<int32_t>(ws, L.inv);
     const int pairs = dims.B * dims.k;
-    const bool dispatch = dims.B > DISPATCH_MIN;
+    const bool dispatch = product_dispatch(dims);
     const int rows = dispatch ? pairs : dims.B, box = product_box_rows(dims);
     ProductMaps maps;
     if (!encode_phase_maps(&maps.phase[0], xq, rows, box, w.Wgate, w.Wup, dims.E, dims.d_ff, dims.d) ||

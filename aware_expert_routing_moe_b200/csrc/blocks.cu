@@ -9,12 +9,12 @@
 // the block's scale, to fp32 accumulators in the registers of eight epilogue
 // warps; several TMEM buffers let the MMAs of the next blocks run meanwhile.
 //
-// Few entries (up to 64 a tile): the weights are the MMA's M (two MMAs of
-// 128 rows), the entries its N (16 to 64).  An MMA then costs what its
+// Few entries (up to 16 a tile): the weights are the MMA's M (two MMAs of
+// 128 rows), the entries its N.  An MMA then costs what its
 // entries cost: with the entries as a half-empty M of 128 the decode kernels
 // drew 990 W and lost a sixth of their speed to the power cap (8 tokens,
 // Qwen3-235B shape, back to back: 174 us against 150 in a short run).  A
-// thread holds one weight row of both matrices for up to 32 entries.
+// thread holds one weight row of both matrices for 8 entries.
 // Many entries (up to 128 a tile): the entries are M (TMEM lanes), the 256
 // weight rows N.  An entry's scale is then one register, and SwiGLU, the
 // largest magnitude of a block of h and its rounding to e4m3 stay inside a
@@ -44,7 +44,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
-constexpr int TILE_MANY = 128, TILE_FEW = 64, TILE_TINY = 16;  // list entries per tile
+constexpr int TILE_MANY = 128, TILE_FEW = 16;  // list entries per tile
 constexpr int TILE_N = 256;       // weight rows per tile (128 + 128 for gate/up)
 constexpr int W_STAGE = TILE_N * BLK;  // weight bytes of a stage: 256 rows x 128 columns
 constexpr int EPI_WARPS = 8;
@@ -60,25 +60,27 @@ constexpr int SGROUP = 4;         // column blocks whose scales are copied toget
 constexpr int SCALES = 3;         // such groups in flight
 constexpr int TILES = 2;          // tiles claimed ahead
 constexpr int PUBS = 4;           // tiles claimed and not yet published, at most
-// Entries of an expert, on average, up to which tiles are of 64 (expert FFN,
-// d 2048, d_ff 1024, 64 experts: 8 entries 79 against 84 us with tiles of
-// 128, 16 entries 88 and 87.5, 32 entries 101 and 92).
-constexpr int FEW_ENTRIES = 16;
+// Tiles are of 16 entries up to FEW_AVERAGE entries an expert on average
+// (expert FFN, d 2048, d_ff 1024, 64 experts: 12 entries 78.8 against 85.3 us
+// with tiles of 128, 20 entries 86.2 and 88.8, 24 entries 95.9 and 90.1; of
+// 64 entries, as an N of up to 64, 82.2, 92.6 and 96.4), and where an expert
+// has at most two such tiles (32 tokens, 8 experts: 32.7 against 37.8 us).
+constexpr int FEW_AVERAGE = 20;
 constexpr int BOX_ROWS = 32;      // activation rows per copy where they are consecutive
 constexpr unsigned long long DRAIN_CYCLES = 2000000000ull;  // 1 s
 
 // A kernel for tiles of AR entries: AR activation rows per stage; with few
-// entries a fifth or sixth stage fits, and four TMEM buffers.
+// entries two more stages fit, and four TMEM buffers.
 template <int AR>
 struct Ring {
-    static constexpr bool FEW = AR <= TILE_FEW;
+    static constexpr bool FEW = AR == TILE_FEW;
     static constexpr int A_STAGE = AR * BLK;
     static constexpr int STAGE = W_STAGE + A_STAGE;
-    static constexpr int STAGES = AR == TILE_TINY ? 6 : FEW ? 5 : 4;
+    static constexpr int STAGES = FEW ? 6 : 4;
     static constexpr int OUT_BYTES = FEW ? AR * BLK : EPI_WARPS * OUT_STAGE;  // h of a tile, or a piece a warp
     static constexpr int BOX = AR < BOX_ROWS ? AR : BOX_ROWS;  // rows per copy
     static constexpr int BUFS = FEW ? 4 : 2;          // TMEM buffers
-    static constexpr int BUF_COLS = 512 / BUFS;       // two blocks of 64 entries, or 256 weight rows
+    static constexpr int BUF_COLS = 512 / BUFS;       // two blocks of entries, or 256 weight rows
 };
 
 enum : int { TILE_END = 2 };
@@ -113,10 +115,9 @@ template <int AR>
 constexpr int smem_bytes() {
     return 1024 + Ring<AR>::STAGES * Ring<AR>::STAGE + Ring<AR>::OUT_BYTES + static_cast<int>(sizeof(Ctl));
 }
-static_assert(ST_MAX * K_MAX / TILE_FEW + SE_MAX < 65536, "m-tile numbers are 16 bits");
-static_assert(smem_bytes<TILE_MANY>() <= 232448 - 64 && smem_bytes<TILE_FEW>() <= 232448 - 64 &&
-                  smem_bytes<TILE_TINY>() <= 232448 - 64,
-              "shared memory budget");
+static_assert(ST_MAX * K_MAX / TILE_MANY + SE_MAX < 65536 && (FEW_AVERAGE + TILE_FEW) * SE_MAX / TILE_FEW < 65536,
+              "m-tile numbers are 16 bits");
+static_assert(smem_bytes<TILE_MANY>() <= 232448 - 64 && smem_bytes<TILE_FEW>() <= 232448 - 64, "shared memory budget");
 // ---------------------------------------------------------------- PTX --
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // Time for the bounded waits: SM cycles at the highest clock, so that a limit
@@ -642,11 +643,11 @@ __device__ void issue_role(unsigned char *ring, Ctl *ctl, const ProductArgs &a) 
             const uint32_t d = tmem + buf * R::BUF_COLS;
             if constexpr (R::FEW) {
                 const uint64_t w1 = umma_desc(saddr(ring + st * R::STAGE + W_STAGE / 2));
-                const uint32_t idesc = idesc_e4m3((x.n + 15) & ~15);
+                constexpr int N = TILE_FEW;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {  // 32 columns = 32 bytes each
-                    umma_e4m3(d, w + 2 * s, v + 2 * s, idesc, s > 0);
-                    umma_e4m3(d + TILE_FEW, w1 + 2 * s, v + 2 * s, idesc, s > 0);
+                    umma_e4m3(d, w + 2 * s, v + 2 * s, idesc_e4m3(N), s > 0);
+                    umma_e4m3(d + TILE_FEW, w1 + 2 * s, v + 2 * s, idesc_e4m3(N), s > 0);
                 }
             } else {
 #pragma unroll
@@ -752,11 +753,10 @@ __device__ __forceinline__ int scale_exponent(float top) {
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // Few entries: thread (weight row, entry half) holds the row of both
-// matrices for up to AR / 2 entries.
-template <int AR>
+// matrices for up to 8 entries.
 __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl, const ProductArgs &a) {
-    using R = Ring<AR>;
-    constexpr int HALF = AR / 2;
+    using R = Ring<TILE_FEW>;
+    constexpr int HALF = TILE_FEW / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;
     const int m = quarter * 32 + lane;  // row of either matrix
@@ -773,8 +773,7 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
         if (x.phase == TILE_END) return;
         const ProductPhase &ph = a.phase[x.phase];
         const int kb = (ph.K + BLK - 1) / BLK;
-        const int wide = ((x.n + 15) & ~15) / 2;            // entries of a half
-        const int first = half * wide, n = min(wide, x.n - first);  // the warp's entries (n <= 0: none)
+        const int first = half * HALF, n = min(HALF, x.n - first);  // the warp's entries (n <= 0: none)
         const uint32_t tbase = ctl->tmem + (static_cast<uint32_t>(quarter * 32) << 16) + first;
         float c0[HALF], c1[HALF];
 #pragma unroll
@@ -791,17 +790,14 @@ __device__ __forceinline__ void epilogue_few(unsigned char *out_stage, Ctl *ctl,
             tc_fence_after();
             const float w0 = ctl->wscale[sc][0][j % SGROUP], w1 = ctl->wscale[sc][1][j % SGROUP];
             const float *as = reinterpret_cast<const float *>(&ctl->scale[sc][first]) + j % SGROUP;
+            if (n > 0) {
+                float u[HALF], v[HALF];
+                tmem_ld8x2(tbase + buf * R::BUF_COLS, tbase + buf * R::BUF_COLS + TILE_FEW, u, v);
 #pragma unroll
-            for (int q = 0; q < HALF / 8; ++q) {
-                if (q * 8 < n) {
-                    float u[8], v[8];
-                    tmem_ld8x2(tbase + buf * R::BUF_COLS + q * 8, tbase + buf * R::BUF_COLS + TILE_FEW + q * 8, u, v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float f = as[(q * 8 + i) * SGROUP];
-                        c0[q * 8 + i] = fmaf(u[i], f * w0, c0[q * 8 + i]);
-                        c1[q * 8 + i] = fmaf(v[i], f * w1, c1[q * 8 + i]);
-                    }
+                for (int i = 0; i < HALF; ++i) {
+                    const float f = as[i * SGROUP];
+                    c0[i] = fmaf(u[i], f * w0, c0[i]);
+                    c1[i] = fmaf(v[i], f * w1, c1[i]);
                 }
             }
             tc_fence_before();
@@ -1023,7 +1019,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     tc_fence_after();
     if (warp < EPI_WARPS) {
         if constexpr (!R::FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
-        if constexpr (R::FEW) epilogue_few<AR>(out_stage, ctl, a);
+        if constexpr (R::FEW) epilogue_few(out_stage, ctl, a);
         else epilogue_many(out_stage, ctl, a);
     } else {
         if constexpr (!R::FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
@@ -1092,22 +1088,20 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
 
 }  // namespace
 
-// Tiles of 16 entries where no expert can have more, of 64 up to FEW_ENTRIES
-// an expert on average, else of 128.
 int product_tile_entries(const moe_dims_t &d) {
     const long long pairs = static_cast<long long>(d.B) * d.k, experts = d.E < pairs ? d.E : pairs;
-    return d.B <= TILE_TINY ? TILE_TINY : pairs <= FEW_ENTRIES * experts ? TILE_FEW : TILE_MANY;
+    return d.B <= 2 * TILE_FEW || pairs <= FEW_AVERAGE * experts ? TILE_FEW : TILE_MANY;
 }
-
+// Large tiles take their rows from copies in list order; small ones gather
+// them by token, four at a time.
+bool product_dispatch(const moe_dims_t &d) { return product_tile_entries(d) == TILE_MANY; }
 int product_box_rows(const moe_dims_t &d) {
     const int n = product_tile_entries(d);
     return n < BOX_ROWS ? n : BOX_ROWS;
 }
 
 cudaError_t launch_product(const ProductMaps &maps, const ProductArgs &a, cudaStream_t s) {
-    return a.tile_entries == TILE_TINY  ? launch_ar<TILE_TINY>(maps, a, s)
-           : a.tile_entries == TILE_FEW ? launch_ar<TILE_FEW>(maps, a, s)
-                                        : launch_ar<TILE_MANY>(maps, a, s);
+    return a.tile_entries == TILE_FEW ? launch_ar<TILE_FEW>(maps, a, s) : launch_ar<TILE_MANY>(maps, a, s);
 }
 
 }  // namespace moe

@@ -26,11 +26,6 @@ struct BlocksControl {
 };
 static_assert(sizeof(BlocksControl) <= MOE_GEMM_WORKSPACE_BYTES, "control segment does not fit");
 
-// Batches above DISPATCH_MIN tokens have each list entry's activation row
-// copied to its place in the lists, so that a tile's rows are one box; up to
-// it the rows are gathered by token.
-constexpr int DISPATCH_MIN = 64;
-
 struct BlocksWs {
     size_t xq, xs, hq, hs, yp, counts, inv, total;
     size_t n_counts;  // cnt [B], then done [m-tiles]
@@ -50,6 +45,9 @@ struct ProductMaps {
 };
 int product_box_rows(const moe_dims_t &d);
 int product_tile_entries(const moe_dims_t &d);  // list entries per tile
+// Whether the expert FFN copies each entry's activation row to its place in
+// the lists (else the rows are gathered by token).
+bool product_dispatch(const moe_dims_t &d);
 bool encode_phase_maps(PhaseMaps *m, const void *a, uint64_t a_rows, int box_rows, const void *b0, const void *b1,
                        uint64_t E, uint64_t rows, uint64_t K);
 
