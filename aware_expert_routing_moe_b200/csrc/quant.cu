@@ -10,6 +10,10 @@
 // the largest e4m3 value), 1 for a block of zeros.  Dividing by a power of
 // two is exact, so the only rounding is the one to e4m3 (nearest even) and
 // the result is fixed bit by bit, whatever computes it.
+//
+// Bound by HBM: each value is read once and a byte written.  Measured: 4096
+// x 2048 bf16 rows 5.1 us (25.4 MB, 5.0 TB/s); 128 matrices of 768 x 2048
+// bf16 103 us (604 MB, 5.9 TB/s, 89 % of the measured copy rate).
 #include <cuda_bf16.h>
 
 #include "blocks.h"

@@ -19,6 +19,12 @@
 // random tokens, and every exact tie).  Without a bias, and with groups
 // valued by their best expert, the logits rank (a score is monotone in its
 // logit) and no score but the chosen ones is computed.
+//
+// Bound by instructions: about 1900 a token with 256 experts in 8 groups
+// (scores 460, groups 390, the k + 1 rounds 370).  Measured: 1 token 8.5 us,
+// 77 tokens 9.3 us, 8192 tokens 39 us (choice 25, lists 10).  With fp32
+// scores and fp64 only for close calls a long batch took as long: some token
+// of it always needed fp64, at the latency of the whole fp64 path.
 #include <cfloat>
 #include <cmath>
 
