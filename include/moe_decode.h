@@ -473,8 +473,9 @@ void moe_set_wait_limit_ns(uint64_t ns);
 
 /* Synchronises `stream`, then reads and clears the error word that kernels
  * of earlier calls using this workspace may have set (a bounded wait that
- * ran out, or inconsistent token lists); works for the layer workspace and
- * for the channel path's workspace alike (both start with the word).  Returns MOE_OK, MOE_ERR_INTERNAL or MOE_ERR_CUDA. */
+ * ran out, or inconsistent token lists); works for the workspace of every
+ * entry point alike (all start with the word).  Returns MOE_OK,
+ * MOE_ERR_INTERNAL or MOE_ERR_CUDA. */
 moe_status_t moe_check_error(void *ws, size_t ws_bytes, void *stream);
 
 /* Static description of a status code (never NULL). */
