@@ -10,11 +10,11 @@
 // warps; several TMEM buffers let the MMAs of the next blocks run meanwhile.
 //
 // Few entries (up to 16 a tile): the weights are the MMA's M (two MMAs of
-// 128 rows), the entries its N.  An MMA then costs what its
-// entries cost: with the entries as a half-empty M of 128 the decode kernels
-// drew 990 W and lost a sixth of their speed to the power cap (8 tokens,
-// Qwen3-235B shape, back to back: 174 us against 150 in a short run).  A
-// thread holds one weight row of both matrices for 8 entries.
+// 128 rows), the entries its N.  An MMA then costs what its entries cost:
+// with the entries as a half-empty M of 128 the decode kernels drew 990 W and
+// lost a sixth of their speed to the power cap (8 tokens, Qwen3-235B shape,
+// back to back: 174 us against 150 in a short run).  A thread holds one
+// weight row of both matrices for 8 entries.
 // Many entries (up to 128 a tile): the entries are M (TMEM lanes), the 256
 // weight rows N.  An entry's scale is then one register, and SwiGLU, the
 // largest magnitude of a block of h and its rounding to e4m3 stay inside a
@@ -28,13 +28,12 @@
 // started.  The last CTA puts the counters back to zero.
 //
 // Roles: warps 0-7 epilogue; warp 8 weights (TMA boxes; they do not wait for
-// the tile's activations); warp 9 MMAs; warp 10 activation rows (boxes of
-// 32 where they are consecutive, else gathered four at a time) and the scales of each column
-// block, copied to a ring of their own, so that no global load latency sits
-// in the epilogue's loop; warp 11 claims tiles and
-// publishes finished ones.  Every wait is bounded; past
-// the limit the CTA records an error, lets its copies and MMAs land and
-// leaves.
+// the tile's activations); warp 9 MMAs; warp 10 activation rows (boxes of 32
+// where they are consecutive, else gathered four at a time) and the scales of
+// each column block, copied to a ring of their own, so that no global load
+// latency sits in the epilogue's loop; warp 11 claims tiles and publishes
+// finished ones.  Every wait is bounded; past the limit the CTA records an
+// error, lets its copies and MMAs land and leaves.
 //
 // What bounds it, measured.  Few entries: HBM.  Expert FFN, Qwen3-30B shape,
 // 16 tokens: 64 us for 321 MB (58 of it this kernel, 312 MB read, tensor
