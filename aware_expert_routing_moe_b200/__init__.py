@@ -12,9 +12,15 @@ Entry points mirror the C ABI in include/moe_decode.h:
 general router ``moe_route_scored``; the block-scaled 8-bit operators
 ``moe_quantize_blocks``, ``moe_expert_gemm_blocks`` and
 ``moe_expert_ffn_blocks``.
+
+A call runs on ``stream`` (a torch stream or a raw handle; default: the
+current stream).  Workspaces, outputs and lists that the caller leaves out are
+made on that stream, as under ``torch.cuda.stream(stream)``; a workspace that
+is passed is used on one stream at a time.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -173,6 +179,27 @@ def _stream(stream):
     return int(stream)
 
 
+def _on(stream, dev: int):
+    """Context in which a call on `stream` makes its own tensors (workspace,
+    outputs, lists).  They belong to that stream: a workspace is zero-filled
+    in order with the kernels that use it, and memory that is freed while
+    they run is handed to nothing but later work of the same stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)  # (ExternalStream takes 0 for a new stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def _made(stream, t, make, *args, **kwargs):
+    """make(..., device=t's) for a call on `stream`."""
+    if stream is None:
+        return make(*args, device=t.device, **kwargs)
+    with _on(stream, t.get_device()):
+        return make(*args, device=t.device, **kwargs)
+
+
 def dims(B: int, d: int, E: int, k: int, d_ff: int) -> Dims:
     return Dims(B, d, E, k, d_ff)
 
@@ -205,10 +232,10 @@ def moe_route(x, Wg, bias, k: int, out=None, stream=None):
     B, d = x.shape
     E = Wg.shape[0]
     if out is None:
-        out = (torch.empty(B, E, dtype=torch.float32, device=x.device),
-               torch.empty(B, E, dtype=torch.float32, device=x.device),
-               torch.empty(B, k, dtype=torch.int32, device=x.device),
-               torch.empty(B, k, dtype=torch.float32, device=x.device))
+        out = (_made(stream, x, torch.empty, B, E, dtype=torch.float32),
+               _made(stream, x, torch.empty, B, E, dtype=torch.float32),
+               _made(stream, x, torch.empty, B, k, dtype=torch.int32),
+               _made(stream, x, torch.empty, B, k, dtype=torch.float32))
     logits, probs, ti, tw = out
     st = load_library().moe_route(_ptr(x), _ptr(Wg), _ptr(bias), Dims(B, d, E, k, 0), _ptr(logits),
                                   _ptr(probs), _ptr(ti), _ptr(tw), _stream(stream))
@@ -222,10 +249,10 @@ def moe_reselect(logits, probs, k: int, mode: int, k0: int = 0, budget: int = 0,
     request (hierarchical XShare)."""
     B, E = logits.shape
     if out is None:
-        out = (torch.empty(B, k, dtype=torch.int32, device=logits.device),
-               torch.empty(B, k, dtype=torch.float32, device=logits.device))
+        out = (_made(stream, logits, torch.empty, B, k, dtype=torch.int32),
+               _made(stream, logits, torch.empty, B, k, dtype=torch.float32))
     if lists is None:
-        lists = alloc_lists(B, E, k, logits.device)
+        lists = _made(stream, logits, alloc_lists, B, E, k)
     sel, w = out
     st = load_library().moe_reselect(_ptr(logits), _ptr(probs), Dims(B, 0, E, k, 0),
                                      Rule(mode, k0, budget, group),
@@ -239,7 +266,7 @@ def moe_expert_ffn(x, Wgate, Wup, Wdown, lists: dict, k: int, ws, y=None, stream
     B, d = x.shape
     E, F, _ = Wgate.shape
     if y is None:
-        y = torch.empty(B, d, dtype=torch.float32, device=x.device)
+        y = _made(stream, x, torch.empty, B, d, dtype=torch.float32)
     st = load_library().moe_expert_ffn(_ptr(x), _ptr(Wgate), _ptr(Wup), _ptr(Wdown), Dims(B, d, E, k, F),
                                        _lists(lists), _ptr(y), _ptr(ws), ws.numel() * ws.element_size()
                                        if isinstance(ws, torch.Tensor) else 0, _stream(stream))
@@ -254,9 +281,9 @@ def moe_layer_decode(x, Wg, bias, Wgate, Wup, Wdown, k: int, mode: int, k0: int 
     B, d = x.shape
     E, F, _ = Wgate.shape
     if ws is None:
-        ws = new_workspace(B, d, E, k, F, x.device)
+        ws = _made(stream, x, new_workspace, B, d, E, k, F)
     if y is None:
-        y = torch.empty(B, d, dtype=torch.float32, device=x.device)
+        y = _made(stream, x, torch.empty, B, d, dtype=torch.float32)
     st = load_library().moe_layer_decode(
         _ptr(x), _ptr(Wg), _ptr(bias), _ptr(Wgate), _ptr(Wup), _ptr(Wdown), Dims(B, d, E, k, F),
         Rule(mode, k0, budget, group), _ptr(y), _ptr(sel_idx), _ptr(sel_w), _ptr(n_active), _ptr(ws),
@@ -279,7 +306,7 @@ def moe_decode_stack(xs, layers, k: int, mode: int, k0: int = 0, budget: int = 0
     _, B, d = xs.shape
     E, F, _ = layers[0][2].shape
     if ws is None:
-        ws = new_workspace(B, d, E, k, F, xs.device)
+        ws = _made(stream, xs, new_workspace, B, d, E, k, F)
     arr = (LayerWeights * n)(*[LayerWeights(_ptr(Wg), _ptr(bias), _ptr(g), _ptr(u), _ptr(dn))
                                for (Wg, bias, g, u, dn) in layers])
     st = load_library().moe_decode_stack(arr, n, Dims(B, d, E, k, F), Rule(mode, k0, budget, group), int(phase),
@@ -294,7 +321,7 @@ def moe_down_channel_major(Wdown, out=None, stream=None):
     transposed per expert (bf16 bits as int16/uint16 tensors)."""
     E, d, F = Wdown.shape
     if out is None:
-        out = torch.empty(E, F, d, dtype=Wdown.dtype, device=Wdown.device)
+        out = _made(stream, Wdown, torch.empty, E, F, d, dtype=Wdown.dtype)
     st = load_library().moe_down_channel_major(_ptr(Wdown), Dims(1, d, E, 1, F), _ptr(out), _stream(stream))
     _check(st, "moe_down_channel_major")
     return out
@@ -314,9 +341,9 @@ def moe_expert_ffn_channels(x, Wgate, Wup, WdownT, sel_idx, sel_w, score, c: int
     if n == 0:
         raise MoeError(4, "moe_channels_workspace_bytes")
     if ws is None:
-        ws = torch.zeros(n, dtype=torch.uint8, device=x.device)
+        ws = _made(stream, x, torch.zeros, n, dtype=torch.uint8)
     if y is None:
-        y = torch.empty(B, d, dtype=torch.float32, device=x.device)
+        y = _made(stream, x, torch.empty, B, d, dtype=torch.float32)
     st = lib.moe_expert_ffn_channels(_ptr(x), _ptr(Wgate), _ptr(Wup), _ptr(WdownT), dims, _ptr(sel_idx),
                                      _ptr(sel_w), _ptr(score), int(c), _ptr(y), _ptr(keep), _ptr(ws),
                                      ws.numel() * ws.element_size(), _stream(stream))
@@ -404,12 +431,12 @@ def moe_route_scored(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, 
     groups, top-k, weights."""
     B, E = logits.shape
     if out is None:
-        out = (torch.empty(B, k, dtype=torch.int32, device=logits.device),
-               torch.empty(B, k, dtype=torch.float32, device=logits.device))
+        out = (_made(stream, logits, torch.empty, B, k, dtype=torch.int32),
+               _made(stream, logits, torch.empty, B, k, dtype=torch.float32))
     if lists is None:
-        lists = alloc_lists(B, E, k, logits.device)
+        lists = _made(stream, logits, alloc_lists, B, E, k)
     if ws is None:
-        ws = new_route_workspace(B, E, k, logits.device)
+        ws = _made(stream, logits, new_route_workspace, B, E, k)
     sel, w = out
     st = (_lib or load_library()).moe_route_scored(
         _ptr(logits), None if bias is None else _buf(bias, 4 * E), _dims(B, 0, E, k, 0),
@@ -427,10 +454,10 @@ def moe_quantize_blocks(x, block_rows: int = 1, q=None, scale=None, stream=None)
     rows, cols = shape[-2:]
     batch = x.numel() // (rows * cols) if rows * cols else 0
     if q is None:
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        q = _made(stream, x, torch.empty, shape, dtype=torch.float8_e4m3fn)
     rb, cb = rows if block_rows == 1 else -(-rows // 128), -(-cols // 128)
     if scale is None:
-        scale = torch.empty((*shape[:-2], rb, cb), dtype=torch.float32, device=x.device)
+        scale = _made(stream, x, torch.empty, (*shape[:-2], rb, cb), dtype=torch.float32)
     st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows,
                                                       _buf(q, batch * rows * cols), _buf(scale, 4 * batch * rb * cb),
                                                       _stream_of(stream, x))
@@ -446,9 +473,9 @@ def moe_expert_gemm_blocks(q, scale, W, Wscale, lists: dict, k: int, ws=None, y=
     B, d = q.shape
     E, F, _ = W.shape
     if ws is None:
-        ws = new_gemm_workspace(q.device)
+        ws = _made(stream, q, new_gemm_workspace)
     if y is None:
-        y = torch.empty(B * k, F, dtype=y_dtype, device=q.device)
+        y = _made(stream, q, torch.empty, B * k, F, dtype=y_dtype)
     cb, rb = -(-d // 128), -(-F // 128)
     st = (_lib or load_library()).moe_expert_gemm_blocks(
         _ptr(q), _buf(scale, 4 * B * cb), _buf(W, E * F * d), _buf(Wscale, 4 * E * rb * cb), _dims(B, d, E, k, F),
@@ -465,9 +492,9 @@ def moe_expert_ffn_blocks(x, Wgate, Sgate, Wup, Sup, Wdown, Sdown, lists: dict, 
     B, d = x.shape
     E, F, _ = Wgate.shape
     if ws is None:
-        ws = new_blocks_workspace(B, d, E, k, F, x.device)
+        ws = _made(stream, x, new_blocks_workspace, B, d, E, k, F)
     if y is None:
-        y = torch.empty(B, d, dtype=y_dtype or x.dtype, device=x.device)
+        y = _made(stream, x, torch.empty, B, d, dtype=y_dtype or x.dtype)
     n, ns = E * F * d, 4 * E * -(-F // 128) * -(-d // 128)
     st = (_lib or load_library()).moe_expert_ffn_blocks(
         _ptr(x), _dtype(x),
@@ -485,7 +512,7 @@ def moe_expert_ffn_noalloc(x, Wgate, Wup, Wdown, lists: dict, k: int, y=None, st
     B, d = x.shape
     E, F, _ = Wgate.shape
     if y is None:
-        y = torch.empty(B, d, dtype=torch.float32, device=x.device)
+        y = _made(stream, x, torch.empty, B, d, dtype=torch.float32)
     st = load_library().moe_expert_ffn_noalloc(_ptr(x), _ptr(Wgate), _ptr(Wup), _ptr(Wdown),
                                                Dims(B, d, E, k, F), _lists(lists), _ptr(y), _stream(stream))
     _check(st, "moe_expert_ffn_noalloc")

@@ -1,0 +1,71 @@
+"""The block-scaled operators where they can go wrong: infinities and NaN,
+wide quantisation of ragged columns, mixed types, re-selected lists, damaged
+lists of large tiles, calls on another stream without a workspace, and one
+workspace for all entry points in turn."""
+import numpy as np
+import pytest
+import torch
+
+import aware_expert_routing_moe_b200 as moe
+import block_cases as bc
+from test_gpu_blocks import BF16, F32, _check_ffn, _check_quantized, _choice, _cuda, _ffn_setup, _lists, _values, _weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    moe.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------- streams, workspaces, limits --
+def _held(side):
+    """Keeps the stream busy for some 50 ms."""
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+
+
+def _litter():
+    """Writes over what the current stream's allocator hands out."""
+    return [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in
+            [512, 1024, 4096, 4352, 16384] * 8 + [1 << 16, 1 << 18, 1 << 20, 1 << 21, 1 << 22, 1 << 24]]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("B,E", [(20, 6), (150, 4)])
+def test_calls_on_another_stream_make_their_buffers_there(B, E, raw):
+    # the workspace and the outputs belong to the call's stream: what the
+    # current stream allocates and writes meanwhile is other memory
+    d, k, F = 256, 3, 256
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+    logits = torch.from_numpy(np.random.default_rng(B).standard_normal((B * 10, 32)).astype(np.float32)).cuda()
+    q, s = moe.moe_quantize_blocks(x)
+    n = L["offsets"][-1]
+    want = (moe.moe_expert_ffn_blocks(x, *args, dev, k), moe.moe_expert_gemm_blocks(q, s, args[0], args[1], dev, k)[:n], q, s,
+            *moe.moe_route_scored(logits, 4)[:2])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    to = side.cuda_stream if raw else side
+    for call in range(4):
+        _held(side)
+        if call == 0:
+            got = [moe.moe_expert_ffn_blocks(x, *args, dev, k, stream=to)]
+        elif call == 1:
+            got = [moe.moe_expert_gemm_blocks(q, s, args[0], args[1], dev, k, stream=to)]
+        elif call == 2:
+            got = list(moe.moe_quantize_blocks(x, stream=to))
+        else:
+            got = list(moe.moe_route_scored(logits, 4, stream=to)[:2])
+        litter = _litter()
+        del litter
+        litter = _litter()
+        side.synchronize()
+        torch.cuda.synchronize()
+        for g, w in zip(got, ([want[0]], [want[1]], want[2:4], want[4:])[call]):
+            g = g[:n] if call == 1 else g
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8)), call
