@@ -200,6 +200,13 @@ def _made(stream, t, make, *args, **kwargs):
         return make(*args, device=t.device, **kwargs)
 
 
+def _empty(stream, t, shape, dtype):
+    """_made(torch.empty), short where the call is on the current stream."""
+    if stream is None:
+        return t.new_empty(shape, dtype=dtype)
+    return _made(stream, t, torch.empty, shape, dtype=dtype)
+
+
 def dims(B: int, d: int, E: int, k: int, d_ff: int) -> Dims:
     return Dims(B, d, E, k, d_ff)
 
@@ -364,29 +371,59 @@ def _scoring(score: int, groups: int, top_groups: int, group_best: int, renorm: 
     return Scoring(score, groups, top_groups, group_best, renorm, scale)
 
 
-def _stream_of(stream, t):
-    """Raw handle of the stream a call on tensor t runs on: t must be on the
-    current device."""
-    if stream is not None:
-        return _stream(stream)
+def _device_of(t) -> int:
+    """The current CUDA device, which t (and every tensor of its call) must
+    be on: a kernel of another device cannot read it."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("tensors must be on the current CUDA device")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return dev
 
 
-def _buf(t, nbytes: int):
-    """Pointer of a contiguous tensor of at least nbytes bytes (the library
-    sees no sizes)."""
-    if isinstance(t, torch.Tensor) and t.nbytes < nbytes:
-        raise ValueError(f"tensor of {t.nbytes} bytes where the call's sizes need {nbytes}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# Element types by what the library reads: it sees addresses only.  e4m3
+# values may come as their bits.
+_I32, _F32, _E4M3 = (torch.int32,), (torch.float32,), (torch.float8_e4m3fn, torch.uint8, torch.int8)
+
+
+def _buf(t, n: int, types, dev: int):
+    """Address of a contiguous tensor of at least n elements of one of the
+    types, on device dev (raw addresses pass, for boundary tests)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in types and t.numel() >= n and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        if t.dtype not in types:
+            raise TypeError(f"expected a tensor of {types[0]}, got {t.dtype}")
+        if t.numel() < n:
+            raise ValueError(f"tensor of {t.numel()} elements where the call's sizes need {n}")
+        if t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
     return _ptr(t)
 
 
-def _list_bufs(l: dict, B: int, E: int, k: int) -> Lists:
-    pairs = 4 * B * k
-    return Lists(_buf(l["n_active"], 4), _buf(l["active"], 4 * E), _buf(l["offsets"], 4 * E + 4), _buf(l["tok"], pairs),
-                 _buf(l["w"], pairs))
+def _weight(w, scale, E: int, rows: int, cols: int, dev: int):
+    """Addresses of e4m3 matrices [E][rows][cols] and their block scales."""
+    if w.shape != (E, rows, cols):
+        raise ValueError(f"weights of shape {tuple(w.shape)} where the call's sizes need {(E, rows, cols)}")
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    if scale.ndim == 3 and scale.shape != (E, rb, cb):
+        raise ValueError(f"weight scales of shape {tuple(scale.shape)} where the call's sizes need {(E, rb, cb)}")
+    return _buf(w, E * rows * cols, _E4M3, dev), _buf(scale, E * rb * cb, _F32, dev)
+
+
+def _list_bufs(l: dict, B: int, E: int, k: int, dev: int) -> Lists:
+    return Lists(_buf(l["n_active"], 1, _I32, dev), _buf(l["active"], E, _I32, dev), _buf(l["offsets"], E + 1, _I32, dev),
+                 _buf(l["tok"], B * k, _I32, dev), _buf(l["w"], B * k, _F32, dev))
+
+
+def _workspace(ws, dev: int):
+    """Address and bytes of a workspace."""
+    if ws.get_device() != dev:
+        raise ValueError("tensors must be on the current CUDA device")
+    return _ptr(ws), ws.nbytes
 
 
 def _dtype(t) -> int:
@@ -394,10 +431,6 @@ def _dtype(t) -> int:
     if code is None:
         raise TypeError("expected a float32 or bfloat16 tensor")
     return code
-
-
-def _bytes(ws) -> int:
-    return ws.numel() * ws.element_size()
 
 
 def _new_bytes(n: int, where: str, device) -> torch.Tensor:
@@ -430,18 +463,18 @@ def moe_route_scored(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, 
     fp32: softmax or sigmoid scores, a bias that steers the choice, expert
     groups, top-k, weights."""
     B, E = logits.shape
+    dev = _device_of(logits)
     if out is None:
-        out = (_made(stream, logits, torch.empty, B, k, dtype=torch.int32),
-               _made(stream, logits, torch.empty, B, k, dtype=torch.float32))
+        out = _empty(stream, logits, (B, k), torch.int32), _empty(stream, logits, (B, k), torch.float32)
     if lists is None:
         lists = _made(stream, logits, alloc_lists, B, E, k)
     if ws is None:
         ws = _made(stream, logits, new_route_workspace, B, E, k)
     sel, w = out
     st = (_lib or load_library()).moe_route_scored(
-        _ptr(logits), None if bias is None else _buf(bias, 4 * E), _dims(B, 0, E, k, 0),
-        _scoring(score, groups, top_groups, group_best, int(renorm), float(scale)), _buf(sel, 4 * B * k),
-        _buf(w, 4 * B * k), _list_bufs(lists, B, E, k), _ptr(ws), _bytes(ws), _stream_of(stream, logits))
+        _buf(logits, B * E, _F32, dev), None if bias is None else _buf(bias, E, _F32, dev), _dims(B, 0, E, k, 0),
+        _scoring(score, groups, top_groups, group_best, int(renorm), float(scale)), _buf(sel, B * k, _I32, dev),
+        _buf(w, B * k, _F32, dev), _list_bufs(lists, B, E, k, dev), *_workspace(ws, dev), _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "moe_route_scored")
     return sel, w, lists
 
@@ -453,14 +486,17 @@ def moe_quantize_blocks(x, block_rows: int = 1, q=None, scale=None, stream=None)
     shape = x.shape
     rows, cols = shape[-2:]
     batch = x.numel() // (rows * cols) if rows * cols else 0
+    code = _dtype(x)
+    dev = _device_of(x)
     if q is None:
-        q = _made(stream, x, torch.empty, shape, dtype=torch.float8_e4m3fn)
+        q = (torch.empty_like(x, dtype=torch.float8_e4m3fn) if stream is None  # (the shortest)
+             else _empty(stream, x, shape, torch.float8_e4m3fn))
     rb, cb = rows if block_rows == 1 else -(-rows // 128), -(-cols // 128)
     if scale is None:
-        scale = _made(stream, x, torch.empty, (*shape[:-2], rb, cb), dtype=torch.float32)
-    st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), _dtype(x), batch, rows, cols, block_rows,
-                                                      _buf(q, batch * rows * cols), _buf(scale, 4 * batch * rb * cb),
-                                                      _stream_of(stream, x))
+        scale = _empty(stream, x, (*shape[:-2], rb, cb), torch.float32)
+    st = (_lib or load_library()).moe_quantize_blocks(_ptr(x), code, batch, rows, cols, block_rows,
+                                                      _buf(q, batch * rows * cols, _E4M3, dev),
+                                                      _buf(scale, batch * rb * cb, _F32, dev), _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "moe_quantize_blocks")
     return q, scale
 
@@ -472,15 +508,16 @@ def moe_expert_gemm_blocks(q, scale, W, Wscale, lists: dict, k: int, ws=None, y=
     128)][ceil(d / 128)].  Rows past the last list entry keep what y held."""
     B, d = q.shape
     E, F, _ = W.shape
+    dev = _device_of(q)
     if ws is None:
         ws = _made(stream, q, new_gemm_workspace)
     if y is None:
-        y = _made(stream, q, torch.empty, B * k, F, dtype=y_dtype)
-    cb, rb = -(-d // 128), -(-F // 128)
+        y = _empty(stream, q, (B * k, F), y_dtype)
+    code = _dtype(y)
     st = (_lib or load_library()).moe_expert_gemm_blocks(
-        _ptr(q), _buf(scale, 4 * B * cb), _buf(W, E * F * d), _buf(Wscale, 4 * E * rb * cb), _dims(B, d, E, k, F),
-        _list_bufs(lists, B, E, k), _buf(y, B * k * F * y.element_size()), _dtype(y), _ptr(ws), _bytes(ws),
-        _stream_of(stream, q))
+        _buf(q, B * d, _E4M3, dev), _buf(scale, B * -(-d // 128), _F32, dev), *_weight(W, Wscale, E, F, d, dev),
+        _dims(B, d, E, k, F), _list_bufs(lists, B, E, k, dev), _buf(y, B * k * F, (y.dtype,), dev), code,
+        *_workspace(ws, dev), _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "moe_expert_gemm_blocks")
     return y
 
@@ -491,16 +528,19 @@ def moe_expert_ffn_blocks(x, Wgate, Sgate, Wup, Sup, Wdown, Sdown, lists: dict, 
     FFN of moe_expert_ffn on block-scaled e4m3 weights; x fp32 or bf16."""
     B, d = x.shape
     E, F, _ = Wgate.shape
+    x_code = _dtype(x)
+    dev = _device_of(x)
     if ws is None:
         ws = _made(stream, x, new_blocks_workspace, B, d, E, k, F)
     if y is None:
-        y = _made(stream, x, torch.empty, B, d, dtype=y_dtype or x.dtype)
-    n, ns = E * F * d, 4 * E * -(-F // 128) * -(-d // 128)
+        y = _empty(stream, x, (B, d), y_dtype or x.dtype)
+    code = _dtype(y)
     st = (_lib or load_library()).moe_expert_ffn_blocks(
-        _ptr(x), _dtype(x),
-        BlockWeights(_buf(Wgate, n), _buf(Sgate, ns), _buf(Wup, n), _buf(Sup, ns), _buf(Wdown, n), _buf(Sdown, ns)),
-        _dims(B, d, E, k, F), _list_bufs(lists, B, E, k), _buf(y, B * d * y.element_size()), _dtype(y), _ptr(ws),
-        _bytes(ws), _stream_of(stream, x))
+        _ptr(x), x_code,
+        BlockWeights(*_weight(Wgate, Sgate, E, F, d, dev), *_weight(Wup, Sup, E, F, d, dev),
+                     *_weight(Wdown, Sdown, E, d, F, dev)),
+        _dims(B, d, E, k, F), _list_bufs(lists, B, E, k, dev), _buf(y, B * d, (y.dtype,), dev), code,
+        *_workspace(ws, dev), _raw_stream(dev) if stream is None else _stream(stream))
     _check(st, "moe_expert_ffn_blocks")
     return y
 
