@@ -17,7 +17,11 @@ inline int blocks_of(int n) { return (n + BLK - 1) / BLK; }
 inline int scale_pitch(int cols) { return (blocks_of(cols) + 3) / 4 * 4; }
 
 // Control segment at the start of every workspace of these operators: the
-// error word first (moe_check_error), then what a call counts in.
+// error word first (moe_check_error), then what a call counts in.  The layer
+// path's Counters start at the same place: all four words are zero between
+// calls there too, so one workspace may serve both in turn, as long as
+// nothing else is kept in, or written to, the first
+// MOE_GEMM_WORKSPACE_BYTES.
 struct BlocksControl {
     int32_t error;
     int32_t next_tile, exits;  // product kernel: tiles claimed, CTAs finished (zero between calls)

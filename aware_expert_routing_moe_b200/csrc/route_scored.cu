@@ -49,6 +49,12 @@ int run_tokens(int B) {
     return SUB * ((subs + RUNS_MAX - 1) / RUNS_MAX);
 }
 
+// The histograms of a workspace start behind what any entry point keeps from
+// call to call in it.
+constexpr size_t HIST_OFFSET = MOE_GEMM_WORKSPACE_BYTES;
+static_assert(sizeof(Counters) <= HIST_OFFSET && sizeof(BlocksControl) <= HIST_OFFSET, "kept counters");
+static_assert(sizeof(BlocksControl) % 256 == 0, "workspace sizes are multiples of 256 bytes");
+
 // Counts of a run: whole 16-byte pieces.
 __host__ __device__ constexpr int hist_pitch(int E) { return (E + 7) / 8 * 8; }
 
@@ -565,7 +571,7 @@ cudaError_t launch_choose(const RouteArgs &a, cudaStream_t s) {
 
 size_t route_ws_bytes(const moe_dims_t &d) {
     const size_t run = run_tokens(d.B), runs = (d.B + run - 1) / run;
-    return (sizeof(BlocksControl) + (d.B <= ONE_LAUNCH ? 0 : runs * hist_pitch(d.E) * 2) + 255) / 256 * 256;
+    return d.B <= ONE_LAUNCH ? sizeof(BlocksControl) : (HIST_OFFSET + runs * hist_pitch(d.E) * 2 + 255) / 256 * 256;
 }
 
 cudaError_t launch_route_scored(const float *logits, const float *bias, const moe_dims_t &d,
@@ -585,7 +591,7 @@ cudaError_t launch_route_scored(const float *logits, const float *bias, const mo
     a.sel_idx = sel_idx;
     a.sel_w = sel_w;
     a.ticket = &control->ticket;
-    a.hist = reinterpret_cast<uint16_t *>(control + 1);
+    a.hist = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(ws) + HIST_OFFSET);
     a.lists = l;
     cudaError_t err = a.E <= 32    ? launch_choose<1>(a, s)
                       : a.E <= 64  ? launch_choose<2>(a, s)

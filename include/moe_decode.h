@@ -41,6 +41,9 @@
  *    a CUDA error, or a device error reported by moe_check_error, zero it
  *    again before reusing it.  Calls that share one workspace must not
  *    overlap in time on the device (same stream, or ordered by events).
+ *    One workspace, as large as the largest needs, may serve all entry
+ *    points in turn, except moe_expert_ffn_channels: that one needs a
+ *    workspace of its own.
  *  - Limits: 1 <= B <= 256, 1 <= k <= 16, k <= E <= 256, d % 64 == 0,
  *    64 <= d <= 16384, d_ff % 64 == 0, 64 <= d_ff <= 8192.  moe_route reads
  *    B, d, E, k of the dims (d_ff is ignored); moe_reselect reads B, E, k.
@@ -129,8 +132,10 @@ typedef struct {
     float *w;
 } moe_lists_t;
 
-/* Bytes of device workspace every entry point below may use for `dims`
- * (one size serves all of them).  Returns 0 if dims are invalid. */
+/* Bytes of device workspace moe_expert_ffn, moe_layer_decode and
+ * moe_decode_stack may use for `dims` (one size serves all of them; the
+ * other entry points have size functions of their own).  Returns 0 if dims
+ * are invalid. */
 size_t moe_workspace_bytes(moe_dims_t dims);
 
 /* Router ("Router Caching and Optimization", "Analyzing Router Inference

@@ -69,3 +69,29 @@ def test_calls_on_another_stream_make_their_buffers_there(B, E, raw):
         for g, w in zip(got, ([want[0]], [want[1]], want[2:4], want[4:])[call]):
             g = g[:n] if call == 1 else g
             assert torch.equal(g.view(torch.uint8), w.view(torch.uint8)), call
+
+
+def test_one_workspace_serves_the_layer_the_router_and_the_experts_in_turn():
+    B, d, E, k, F = 40, 256, 32, 4, 128
+    rng = np.random.default_rng(31)
+    t = lambda *n: torch.from_numpy((rng.standard_normal(n) * 0.05).astype(np.float32)).cuda()
+    x, Wg = t(B, d) * 20, t(E, d)
+    bf = [m.bfloat16().view(torch.int16) for m in (t(E, F, d), t(E, F, d), t(E, d, F))]
+    q8 = [u for m in (t(E, F, d), t(E, F, d), t(E, d, F)) for u in moe.moe_quantize_blocks(m, 128)]
+    logits = t(5000, E) * 20
+    ws = torch.zeros(max(moe.moe_workspace_bytes(B, d, E, k, F), moe.new_route_workspace(5000, E, k).numel(),
+                         moe.new_blocks_workspace(B, d, E, k, F).numel()), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(3):
+        sel = torch.empty(B, k, dtype=torch.int32, device="cuda")
+        y = moe.moe_layer_decode(x, Wg, None, *bf, k, moe.MOE_RESELECT_OEA, k0=2, ws=ws, sel_idx=sel)
+        assert moe.moe_check_error(ws) == 0
+        lsel, lw, _ = moe.moe_route_scored(logits, k, ws=ws)
+        small, _, lists = moe.moe_route_scored(logits[:B].contiguous(), k, ws=ws)
+        y8 = moe.moe_expert_ffn_blocks(x, *q8, lists, k, ws=ws)
+        assert moe.moe_check_error(ws) == 0
+        got = [y, sel, lsel, lw, small, y8]
+        first = first or [g.clone() for g in got]
+        assert float((y - first[0]).norm() / y.norm()) < 1e-5  # the layer's fp32 atomics add in any order
+        for g, w in zip(got[1:], first[1:]):
+            assert torch.equal(g, w)
