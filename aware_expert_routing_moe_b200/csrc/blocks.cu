@@ -424,7 +424,9 @@ __device__ void scheduler(Ctl *ctl, const ProductArgs &a) {
             Tile x;
             x.phase = TILE_END;
             x.n = x.ready = 0;
-            if (t < t0) x = tile_at<AR>(t, 0, nbt0, ctl);
+            if (t < 0) {  // a workspace that was not zero-filled
+                if (lane == 0) atomicCAS(a.error, 0, DEV_BAD_LISTS);
+            } else if (t < t0) x = tile_at<AR>(t, 0, nbt0, ctl);
             else if (t < total) x = tile_at<AR>(t - t0, 1, nbt1, ctl);
             int tok[4];
             if (x.phase != TILE_END) {

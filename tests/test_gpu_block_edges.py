@@ -22,6 +22,10 @@ def _lib():
     torch.cuda.synchronize()
 
 
+# ------------------------------------------------------ products and FFN --
+SIZES = [(20, 272, 6, 3, 400), (150, 512, 4, 3, 256), (40, 256, 40, 3, 128)]  # tiles of 16, 128 and 16 entries
+
+
 # ------------------------------------------- streams, workspaces, limits --
 def _held(side):
     """Keeps the stream busy for some 50 ms."""
@@ -95,3 +99,19 @@ def test_one_workspace_serves_the_layer_the_router_and_the_experts_in_turn():
         assert float((y - first[0]).norm() / y.norm()) < 1e-5  # the layer's fp32 atomics add in any order
         for g, w in zip(got[1:], first[1:]):
             assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("B,d,E,k,F", SIZES[:2])
+def test_a_tile_counter_below_zero_is_reported(B, d, E, k, F):
+    # as in a workspace that was never zero-filled: nothing is written out of
+    # place, and the last CTA puts the counter right
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+    ws, guard = moe.new_blocks_workspace(B, d, E, k, F), 16
+    buf = torch.full((B + 2 * guard, d), 3.0, dtype=BF16, device="cuda")
+    ws.view(torch.int32)[1] = -5000
+    moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws, y=buf[guard:guard + B])
+    assert moe.moe_check_error(ws) == 6
+    assert torch.all(buf[:guard] == 3) and torch.all(buf[guard + B:] == 3)
+    y = moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, vals)
