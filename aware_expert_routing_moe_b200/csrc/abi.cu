@@ -197,7 +197,10 @@ ProductArgs product_args(const moe_dims_t &d, const moe_lists_t &l, void *ws) {
     a.error = &c->error;
     a.next_tile = &c->next_tile;
     a.exits = &c->exits;
-    a.wait_ns = wait_limit_ns();
+    // the kernel counts in cycles, two a nanosecond: room for the product
+    constexpr unsigned long long MOST_NS = 1ull << 62;
+    const unsigned long long limit = wait_limit_ns();
+    a.wait_ns = limit < MOST_NS ? limit : MOST_NS;
     a.tile_entries = product_tile_entries(d);
     return a;
 }

@@ -101,6 +101,21 @@ def test_one_workspace_serves_the_layer_the_router_and_the_experts_in_turn():
             assert torch.equal(g, w)
 
 
+@pytest.mark.parametrize("limit", [2 ** 62, 2 ** 63, 2 ** 64 - 1])
+def test_the_longest_wait_limits(limit):
+    L, dev, x, args, vals = _ffn_setup(150, 512, 4, 3, 256, BF16)
+    ws, gws = moe.new_blocks_workspace(150, 512, 4, 3, 256), moe.new_gemm_workspace()
+    q, s = moe.moe_quantize_blocks(x)
+    try:
+        moe.moe_set_wait_limit_ns(limit)
+        y = moe.moe_expert_ffn_blocks(x, *args, dev, 3, ws=ws)
+        moe.moe_expert_gemm_blocks(q, s, args[0], args[1], dev, 3, ws=gws)
+        assert moe.moe_check_error(ws) == 0 and moe.moe_check_error(gws) == 0
+    finally:
+        moe.moe_set_wait_limit_ns(0)
+    _check_ffn(y, x, L, vals)
+
+
 @pytest.mark.parametrize("B,d,E,k,F", SIZES[:2])
 def test_a_tile_counter_below_zero_is_reported(B, d, E, k, F):
     # as in a workspace that was never zero-filled: nothing is written out of
