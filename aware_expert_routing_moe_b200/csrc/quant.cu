@@ -22,6 +22,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned ALL = 0xffffffffu;
+constexpr unsigned INF_BITS = 0x7f800000u;  // magnitude bits of fp32 infinity; NaN above
 // Rows from which a warp takes 2048 (bf16) or 1024 (fp32) columns instead of
 // 512 (4096 x 2048 bf16: 4.65 against 4.99 us).
 constexpr long long WIDE_ROWS = 2048;
@@ -45,8 +46,19 @@ __device__ __forceinline__ unsigned pack4(float a, float b, float c, float d, fl
     return static_cast<unsigned>(lo) | (static_cast<unsigned>(hi) << 16);
 }
 
+// The largest finite magnitude among two (fp32 bits), and x with an infinity
+// made NaN.
+__device__ __forceinline__ unsigned finite_max(unsigned top, unsigned bits) {
+    bits &= 0x7fffffffu;
+    return bits < INF_BITS ? max(top, bits) : top;
+}
+__device__ __forceinline__ unsigned inf_to_nan(unsigned bits) {
+    return (bits & 0x7fffffffu) == INF_BITS ? 0x7fffffffu : bits;
+}
+
 // A lane's 16 columns: raw loads, the largest magnitude, and the four words
-// of e4m3 values.
+// of e4m3 values.  Where the largest magnitude is not finite, `settle` makes
+// infinities NaN and gives the largest finite one.
 template <typename T>
 struct Lane16;
 template <>
@@ -68,6 +80,20 @@ struct Lane16<float> {
                     max(__float_as_uint(v[i].z) & 0x7fffffffu, __float_as_uint(v[i].w) & 0x7fffffffu));
         return t;
     }
+    __device__ __forceinline__ unsigned settle() {
+        unsigned t = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *f[4] = {&v[i].x, &v[i].y, &v[i].z, &v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned b = __float_as_uint(*f[j]);
+                t = finite_max(t, b);
+                *f[j] = __uint_as_float(inf_to_nan(b));
+            }
+        }
+        return t;
+    }
     __device__ __forceinline__ uint4 pack(float inv) const {
         return make_uint4(pack4(v[0].x, v[0].y, v[0].z, v[0].w, inv), pack4(v[1].x, v[1].y, v[1].z, v[1].w, inv),
                           pack4(v[2].x, v[2].y, v[2].z, v[2].w, inv), pack4(v[3].x, v[3].y, v[3].z, v[3].w, inv));
@@ -86,6 +112,20 @@ struct Lane16<__nv_bfloat16> {
         return max(max(max(top2(v[0].x), top2(v[0].y)), max(top2(v[0].z), top2(v[0].w))),
                    max(max(top2(v[1].x), top2(v[1].y)), max(top2(v[1].z), top2(v[1].w))));
     }
+    __device__ __forceinline__ unsigned settle() {
+        unsigned t = 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            unsigned *w[4] = {&v[i].x, &v[i].y, &v[i].z, &v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned lo = *w[j] << 16, hi = *w[j] & 0xffff0000u;
+                t = finite_max(finite_max(t, lo), hi);
+                *w[j] = (inf_to_nan(lo) >> 16) | (inf_to_nan(hi) & 0xffff0000u);
+            }
+        }
+        return t;
+    }
     static __device__ __forceinline__ unsigned pack2(unsigned a, unsigned b, float inv) {
         return pack4(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
                      __uint_as_float(b & 0xffff0000u), inv);
@@ -96,12 +136,42 @@ struct Lane16<__nv_bfloat16> {
     }
 };
 
+// A block's 128 x 128 tile that holds an infinity or NaN, read again (out of
+// line: the kept values would cost a third more registers): row r0 + 32 i,
+// column c of the thread's values at x + 32 i pitch.
+template <typename T>
+__device__ __noinline__ void round_tile(const T *x, uint8_t *q, float *scale, int rows, int pitch, bool inside,
+                                        unsigned *s_top) {
+    Lane16<T> v;
+    unsigned top = 0u;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+        if (inside && 32 * i < rows) {
+            v.load(x + 32ll * i * pitch);
+            top = max(top, v.settle());
+        }
+    top = __reduce_max_sync(ALL, top);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) top = max(top, s_top[i]);
+    const int e = scale_exp(top);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+        if (inside && 32 * i < rows) {
+            v.load(x + 32ll * i * pitch);
+            v.settle();
+            *reinterpret_cast<uint4 *>(q + 32ll * i * pitch) = v.pack(pow2(-e));
+        }
+    if (threadIdx.x == 0) *scale = pow2(e);
+}
+
 // A warp per SPAN * 512 columns of a row: 16 columns a lane and chunk of 512
 // (16-byte loads and one 16-byte store), eight lanes a block of 128, the
 // chunks' loads in flight together.  Scale of row r, block j at
 // scale[r * pitch + j].
 template <typename T, int SPAN>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, unsigned rows, int cols,
+__global__ void __launch_bounds__(256, SPAN > 1 ? 4 : 1) quantize_rows_kernel(const T *__restrict__ x, unsigned rows, int cols,
                                                             unsigned spans, const int32_t *__restrict__ src, int n_src,
                                                             uint8_t *__restrict__ q, float *__restrict__ scale,
                                                             int pitch, int32_t *__restrict__ zero, int n_zero) {
@@ -125,16 +195,23 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
             if (c0 + u * 512 < cols) v[u].load(x + from * cols + c0 + u * 512);
             else v[u].zero();
         }
+        uint8_t *const qr = q + static_cast<long long>(r) * cols;
+        float *const sr = scale + static_cast<long long>(r) * pitch;
 #pragma unroll
         for (int u = 0; u < SPAN; ++u) {
             const int c = c0 + u * 512;
             unsigned top = v[u].top();
 #pragma unroll
             for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(ALL, top, o));
+            if (__any_sync(ALL, top >= INF_BITS)) {  // rare; all lanes together, for the shuffles
+                top = v[u].settle();
+#pragma unroll
+                for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(ALL, top, o));
+            }
             const int e = scale_exp(top);
             if (c < cols) {
-                *reinterpret_cast<uint4 *>(q + static_cast<long long>(r) * cols + c) = v[u].pack(pow2(-e));
-                if ((lane & 7) == 0) scale[static_cast<long long>(r) * pitch + c / BLK] = pow2(e);
+                *reinterpret_cast<uint4 *>(qr + c) = v[u].pack(pow2(-e));
+                if ((lane & 7) == 0) sr[c / BLK] = pow2(e);
             }
         }
         if (b + warps < b) break;  // the counter would wrap
@@ -168,6 +245,11 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, s_top[i]);
+    if (top >= INF_BITS) {  // the same for the whole block
+        const long long at = base + static_cast<long long>(r0) * cols + c;
+        round_tile(x + at, q + at, scale + tile, rows - r0, cols, c < cols, s_top);
+        return;
+    }
     const int e = scale_exp(top);
     const float inv = pow2(-e);
 #pragma unroll

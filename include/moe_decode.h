@@ -47,7 +47,8 @@
  *  - Limits: 1 <= B <= 256, 1 <= k <= 16, k <= E <= 256, d % 64 == 0,
  *    64 <= d <= 16384, d_ff % 64 == 0, 64 <= d_ff <= 8192.  moe_route reads
  *    B, d, E, k of the dims (d_ff is ignored); moe_reselect reads B, E, k.
- *  - Inputs must be finite; NaN or Inf inputs give unspecified results.
+ *  - Inputs must be finite; NaN or Inf inputs give unspecified results,
+ *    except where an entry point says what they give.
  *  - Nothing is thrown across the ABI.
  */
 #ifndef MOE_DECODE_H
@@ -374,7 +375,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype_t;
  * 128 (scale[batch][ceil(rows / 128)][ceil(cols / 128)]).  A block's scale
  * is the smallest power of two s with max|x| <= 448 s (1 for zeros, at
  * least 2^-120), q = x / s rounded to nearest even: the only rounding, so
- * the result is exact bit by bit.  batch, rows >= 1, batch * rows < 2^31,
+ * the result is exact bit by bit.  An infinity or NaN becomes NaN (e4m3 has
+ * no infinity) and does not count in its block's scale.
+ * batch, rows >= 1, batch * rows < 2^31,
  * cols % 16 == 0, 16 <= cols <= 16384 * 4, at most 2^31 - 1 blocks.
  * Needs no workspace. */
 moe_status_t moe_quantize_blocks(const void *x, int32_t type, int64_t batch, int64_t rows, int64_t cols,
@@ -386,10 +389,12 @@ moe_status_t moe_quantize_blocks(const void *x, int32_t type, int64_t batch, int
  * (lists as moe_reselect and moe_route_scored write them; w is not read).
  * One expert that lists every token makes it a plain product.
  *   q[B][d] e4m3 with scale[B][ceil(d / 128)]; W[E][d_ff][d] e4m3 with
- *   Wscale[E][ceil(d_ff / 128)][ceil(d / 128)] (any finite scales);
+ *   Wscale[E][ceil(d_ff / 128)][ceil(d / 128)] (any scales whose products
+ *   with the activations' are finite in fp32);
  *   y[B * k][d_ff] of y_type (moe_dtype_t); rows past the last list entry
  *   are left as they were.
- * Sums are fp32, rounded once at the end.  The result does not depend on
+ * Sums are fp32, rounded once at the end.  NaN in a row of q makes that
+ * entry's y NaN and no other's.  The result does not depend on
  * scheduling.  ws: MOE_GEMM_WORKSPACE_BYTES bytes, 256-byte aligned,
  * zero-filled once (its error word is moe_check_error's). */
 moe_status_t moe_expert_gemm_blocks(const uint8_t *q, const float *scale, const uint8_t *W, const float *Wscale,
@@ -416,9 +421,11 @@ size_t moe_blocks_workspace_bytes(moe_dims_t dims);
  * x[B][d] and h are rounded to e4m3 in blocks of 128 columns as
  * moe_quantize_blocks does (the format's 8-bit operands), sums are fp32,
  * y[B][d] is rounded once.  x_type, y_type: moe_dtype_t.  y is overwritten
- * (0 for a token in no list).  A token's entries are added in list order:
- * the result does not depend on scheduling.  ws: moe_blocks_workspace_bytes
- * bytes, 256-byte aligned, zero-filled once before its first use. */
+ * (0 for a token in no list).  A listed token with an infinity or NaN in x,
+ * or whose h overflows fp32, gets a row of NaN; the others are not touched.
+ * A token's entries are added in list order: the result does not depend on
+ * scheduling.  ws: moe_blocks_workspace_bytes bytes, 256-byte aligned,
+ * zero-filled once before its first use. */
 moe_status_t moe_expert_ffn_blocks(const void *x, int32_t x_type, moe_block_weights_t weights, moe_dims_t dims,
                                    moe_lists_t lists, void *y, int32_t y_type, void *ws, size_t ws_bytes,
                                    void *stream);

@@ -22,8 +22,76 @@ def _lib():
     torch.cuda.synchronize()
 
 
+# ---------------------------------------------------------- quantisation --
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols,block_rows", [(7, 400, 1), (2100, 1040, 1), (300, 272, 128)])
+def test_infinities_and_nan_become_nan(dtype, rows, cols, block_rows):
+    # and the finite values of their blocks are rounded as if they were zeros
+    rng = np.random.default_rng([rows, cols])
+    x = torch.from_numpy(rng.standard_normal((rows, cols)).astype(np.float32)).to(dtype).float().numpy()
+    bad = rng.random((rows, cols)) < 0.002
+    bad[0, :130] = True                  # whole blocks of a row
+    bad[1, 5] = bad[2, 140] = bad[3, cols - 1] = True
+    bad[4] = False
+    kind = rng.integers(0, 3, (rows, cols))
+    kind[1, 5], kind[2, 140], kind[3, cols - 1] = 0, 1, 2
+    dirty = np.where(bad, np.choose(kind, [np.float32(np.inf), np.float32(-np.inf), np.float32(np.nan)]), x)
+    q, s = moe.moe_quantize_blocks(_cuda(dirty.astype(np.float32)).to(dtype), block_rows)
+    rq, rs = bc.quantize(np.where(bad, 0.0, x), block_rows)
+    got = _values(q)
+    assert np.array_equal(np.isnan(got), bad)
+    assert np.array_equal(np.where(bad, 0.0, got), np.where(bad, 0.0, rq))
+    assert np.array_equal(s.double().cpu().numpy(), rs)
+
+
 # ------------------------------------------------------ products and FFN --
+def test_product_keeps_nan_in_its_rows():
+    rng = np.random.default_rng(3)
+    for B, E, k in ((20, 6, 2), (300, 2, 1)):  # tiles of 16 and of 128 entries
+        d, F = 272, 400
+        sel, w = _choice(rng, B, E, k)
+        L, dev = _lists(sel, w, E)
+        x = torch.from_numpy(rng.standard_normal((B, d)).astype(np.float32)).cuda()
+        bad = [1, 7, B - 1]
+        dirty = x.clone()
+        dirty[1, 3], dirty[7, 271], dirty[B - 1, 130] = float("inf"), float("nan"), float("-inf")
+        Wq, Ws, _ = _weights(rng, E, F, d)
+        ys = []
+        for v in (x, dirty):
+            q, s = moe.moe_quantize_blocks(v)
+            ys.append(moe.moe_expert_gemm_blocks(q, s, Wq, Ws, dev, k, y_dtype=F32)[:L["offsets"][-1]])
+        hit = torch.from_numpy(np.isin(L["tok"][:L["offsets"][-1]], bad)).cuda()
+        assert torch.isnan(ys[1][hit]).all() and torch.equal(ys[1][~hit], ys[0][~hit])
+
+
 SIZES = [(20, 272, 6, 3, 400), (150, 512, 4, 3, 256), (40, 256, 40, 3, 128)]  # tiles of 16, 128 and 16 entries
+
+
+@pytest.mark.parametrize("B,d,E,k,F", SIZES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_ffn_of_a_row_that_is_not_finite_is_nan(B, d, E, k, F, dtype, value):
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, dtype)
+    clean = moe.moe_expert_ffn_blocks(x, *args, dev, k)
+    dirty = x.clone()
+    dirty[3, d - 1] = dirty[B - 1, 0] = dirty[B // 2, 140] = value
+    y = moe.moe_expert_ffn_blocks(dirty, *args, dev, k)
+    bad = torch.zeros(B, dtype=torch.bool, device="cuda")
+    bad[[3, B - 1, B // 2]] = True
+    assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("B,d,E,k,F", SIZES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ffn_whose_h_overflows_is_nan(B, d, E, k, F, dtype):
+    # gate and up are about 1e32 each, their product is past fp32
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, dtype)
+    clean = moe.moe_expert_ffn_blocks(x, *args, dev, k)
+    dirty = x.clone()
+    dirty[5] *= 1e30
+    y = moe.moe_expert_ffn_blocks(dirty, *args, dev, k)
+    other = torch.arange(B, device="cuda") != 5
+    assert torch.isnan(y[5]).all() and torch.equal(y[other], clean[other])
 
 
 # ------------------------------------------- streams, workspaces, limits --
