@@ -351,10 +351,8 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int b, const int (&gr
     }
     const double sum = a.rule.renorm ? warp_sum(s) : z;
     if (lane < a.k) {
-        float w = 0.0f;
-        if (mine >= 0 && sum > 0.0)
-            w = sum > 1e-30 && s > 1e-30 ? static_cast<float>(s) / static_cast<float>(sum) * a.rule.scale
-                                         : static_cast<float>(s / sum * static_cast<double>(a.rule.scale));
+        // rounded once, at the end
+        const float w = mine >= 0 && sum > 0.0 ? static_cast<float>(s / sum * static_cast<double>(a.rule.scale)) : 0.0f;
         a.sel_idx[static_cast<size_t>(b) * a.k + lane] = mine;
         a.sel_w[static_cast<size_t>(b) * a.k + lane] = w;
         if (a.runs == 1) {
