@@ -52,3 +52,64 @@ def _check(logits, k, sigmoid, bias=None, groups=1, top_groups=1, best=1, renorm
 def test_weights_are_rounded_once(sigmoid, renorm, scale):
     _check(_logits(150, 96, 1), 8, sigmoid, renorm=renorm, scale=scale)
     _check(_logits(40, 256, 2, 6.0), 16, sigmoid, np.full(256, 0.1, np.float32), renorm=renorm, scale=scale)
+
+
+def test_small_logits_that_fp64_does_tell_apart():
+    # steps of 2^-46: scores 1.4e-14 apart, some sixty fp64 steps
+    l = np.full((2, 32), -1.0, np.float32)
+    l[0, 3:9] = np.arange(6, dtype=np.float32) * np.float32(2.0 ** -46)
+    l[1, 3:9] = -np.arange(6, dtype=np.float32) * np.float32(2.0 ** -46)
+    for sigmoid in (False, True):
+        _check(l, 4, sigmoid)
+        _check(l, 4, sigmoid, np.zeros(32, np.float32))
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (33, 4), (160, 6), (512, 16)])
+@pytest.mark.parametrize("B", [16, 17, 512, 513, 1100])
+@pytest.mark.parametrize("masked", [False, True])
+def test_one_launch_and_two(B, E, k, masked):
+    l = _logits(B, E, 3)
+    if masked:
+        rng = np.random.default_rng([4, B, E])
+        l[rng.random(l.shape) < 0.3] = -np.inf
+        l[rng.random(B) < 0.2] = -np.inf
+        l[0], l[-1] = np.nan, -np.inf
+    _check(l, k, bool(B & 1) != masked)
+
+
+@pytest.mark.parametrize("B", [3, 513, 2000])
+def test_all_tokens_masked(B):
+    sel, _ = _check(np.full((B, 40), -np.inf, np.float32), 5, True)
+    assert np.all(sel == -1)
+
+
+@pytest.mark.parametrize("B", [60, 700])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_logits_of_bf16_precision(B, sigmoid):
+    l = torch.from_numpy(_logits(B, 256, 5)).bfloat16().float().numpy()
+    _check(l, 8, sigmoid)
+    _check(l, 8, sigmoid, None, 8, 3, 1)
+    _check(l, 8, sigmoid, (np.random.default_rng(6).standard_normal(256) * 0.05).astype(np.float32), 8, 4, 2)
+
+
+def test_two_launches_captured_and_replayed():
+    T, E, k = 1500, 64, 6
+    x = torch.from_numpy(_logits(T, E, 7)).cuda()
+    out = (torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda"))
+    lists, ws = moe.alloc_lists(T, E, k), moe.new_route_workspace(T, E, k)
+    call = lambda: moe.moe_route_scored(x, k, out=out, lists=lists, ws=ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for seed in (8, 9):
+        l = _logits(T, E, seed)
+        x.copy_(torch.from_numpy(l))
+        g.replay()
+        torch.cuda.synchronize()
+        rsel, _ = bc.route(l, k, False)
+        assert np.array_equal(out[0].cpu().numpy(), rsel)
+        ref = bc.lists_of(rsel, out[1].cpu().numpy(), E)
+        for n in ("active", "offsets", "tok"):
+            assert np.array_equal(lists[n].cpu().numpy(), ref[n]), n
