@@ -135,10 +135,14 @@ __device__ __forceinline__ double exp_from(float l, float top) {
 }
 __device__ __forceinline__ int round_int(double v) { return __double2loint(v + ROUND); }
 
-// Logits for which fp64 scores keep the order of the logits.
-constexpr float TOP_LOGIT = 16.0f, LOW_LOGIT = -600.0f;
-// Images: 27 bits of value (a unit is 2^-26 of the largest magnitude, at
-// most) over 4 bits of slot.  Rounding moves a value by half a unit, so two
+// Logits for which fp64 scores keep the order of the logits: not near 1 for
+// sigmoid scores, at most 600 below the largest for softmax.  Below
+// TINY_LOGIT neighbouring fp32 values can be nearer than fp64 scores tell
+// (from it on they are 2^-40 apart, and l - top is rounded by 2^-44 at most):
+// close calls among such logits are decided by the scores.
+constexpr float TOP_LOGIT = 16.0f, LOW_LOGIT = -600.0f, TINY_LOGIT = 1.0f / 65536.0f;
+// Images: 28 bits of value (1 to 2^27 + 1; a unit is 2^-26 to 2^-25 of the
+// bound on the values' magnitude) over 4 bits of slot.  Rounding moves a value by half a unit, so two
 // that are more than NEAR units apart are in order; sums of two, SUM_NEAR.
 constexpr int SLOT_BITS = 4, NEAR = 2, SUM_NEAR = 4;
 
@@ -215,60 +219,91 @@ struct Token {
     }
 };
 
-    // The same by the values c (overwritten).
-    template <int NI>
-__device__ __noinline__ int by_value(const RouteArgs &a, double (&c)[NI], double *row) {
-        const int lane = threadIdx.x & 31;
-        const int G = a.rule.groups, per = a.E / G;
-        if (G > 1) {
-            __syncwarp();
+// The scores of logits c (-inf: not to choose from), in their place.
+template <int NI>
+__device__ __forceinline__ void to_scores(double (&c)[NI], bool sig, float shift) {
+    double sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
-            __syncwarp();
-            double b1 = -INFINITY, b2 = -INFINITY;
-            if (lane < G)
-                for (int j = 0; j < per; ++j) {
-                    const double v = row[lane * per + j];
-                    if (v > b1) {
-                        b2 = b1;
-                        b1 = v;
-                    } else if (v > b2) b2 = v;
-                }
-            double value = b1;
-            if (a.rule.group_best == 2 && b2 > -INFINITY) value += b2;
-            unsigned keep = 0;
-            for (int j = 0; j < a.rule.top_groups; ++j) {
-                double v = (keep >> lane) & 1u ? -INFINITY : value;
-                int g = lane;
-                warp_best(v, g);
-                if (v > -INFINITY) keep |= 1u << g;
-            }
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.E && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
-            }
-        }
-        int mine = -1;
-        for (int j = 0; j < a.k; ++j) {
-            double v = -INFINITY;
-            int e = 1 << 20;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (c[i] > v) {
-                    v = c[i];
-                    e = lane + 32 * i;
-                }
-            warp_best(v, e);
-            if (v == -INFINITY) break;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == e) c[i] = -INFINITY;
-            if (lane == j) mine = e;
-        }
-        return mine;
+    for (int i = 0; i < NI; ++i) {
+        if (c[i] == -INFINITY) continue;
+        const float l = static_cast<float>(c[i]);
+        c[i] = sig ? sigmoid(l) : exp_from(l, shift);
+        sum += c[i];
     }
+    if (sig) return;
+    const double inv = 1.0 / warp_sum(sum);  // (not of a token that has no expert: its images are sure)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (c[i] > -INFINITY) c[i] *= inv;
+}
+
+// The same by the values c (overwritten); logits (by_logit) by their scores
+// where a tiny one has another near it.
+template <int NI>
+__device__ __noinline__ int by_value(const RouteArgs &a, double (&c)[NI], double *row, bool by_logit, float shift) {
+    if (by_logit) {
+        bool tiny = false;
+        int near_zero = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const bool near = fabs(c[i]) < TINY_LOGIT;
+            near_zero += near;
+            tiny = tiny || (near && c[i] != 0.0);
+        }
+        if (__any_sync(ALL, tiny) && __reduce_add_sync(ALL, near_zero) > 1)
+            to_scores<NI>(c, a.rule.score == MOE_SCORE_SIGMOID, shift);
+    }
+    const int lane = threadIdx.x & 31;
+    const int G = a.rule.groups, per = a.E / G;
+    if (G > 1) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
+        __syncwarp();
+        double b1 = -INFINITY, b2 = -INFINITY;
+        if (lane < G)
+            for (int j = 0; j < per; ++j) {
+                const double v = row[lane * per + j];
+                if (v > b1) {
+                    b2 = b1;
+                    b1 = v;
+                } else if (v > b2) b2 = v;
+            }
+        double value = b1;
+        if (a.rule.group_best == 2 && b2 > -INFINITY) value += b2;
+        unsigned keep = 0;
+        for (int j = 0; j < a.rule.top_groups; ++j) {
+            double v = (keep >> lane) & 1u ? -INFINITY : value;
+            int g = lane;
+            warp_best(v, g);
+            if (v > -INFINITY) keep |= 1u << g;
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.E && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
+        }
+    }
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double v = -INFINITY;
+        int e = 1 << 20;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (c[i] > v) {
+                v = c[i];
+                e = lane + 32 * i;
+            }
+        warp_best(v, e);
+        if (v == -INFINITY) break;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane + 32 * i == e) c[i] = -INFINITY;
+        if (lane == j) mine = e;
+    }
+    return mine;
+}
 
 __device__ __forceinline__ float clean_logit(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
 
@@ -341,7 +376,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int b, const int (&gr
         double c[NI];  // a copy: the values themselves stay in registers
 #pragma unroll
         for (int i = 0; i < NI; ++i) c[i] = t.c[i];
-        mine = by_value<NI>(a, c, row);
+        mine = by_value<NI>(a, c, row, by_logit, shift);
     }
     // lane j: the score of its expert
     double s = 0.0;

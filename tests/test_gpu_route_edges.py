@@ -54,6 +54,26 @@ def test_weights_are_rounded_once(sigmoid, renorm, scale):
     _check(_logits(40, 256, 2, 6.0), 16, sigmoid, np.full(256, 0.1, np.float32), renorm=renorm, scale=scale)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups,top", [(1, 1), (4, 2)])
+def test_scores_that_fp64_cannot_tell_apart_go_to_the_lower_index(sigmoid, groups, top):
+    # exp(1e-20) and exp(0) are the same fp64 number: with a bias of zeros and
+    # without one the choice is the lower index
+    l = np.full((6, 64), -1.0, np.float32)
+    l[0, 0], l[0, 5] = 0.0, 1e-20
+    l[1, 40], l[1, 3] = 1e-20, -1e-20
+    l[2] = np.linspace(1e-12, 64e-12, 64) * 1e-9
+    l[3, 17], l[3, 16] = 1e-30, 0.0
+    l[4, 9:13] = [2e-19, 1e-38, 1e-45, 3e-19]
+    l[5] = 0.5
+    zero = np.zeros(64, np.float32)
+    for k in (1, 4):
+        a, _ = _check(l, k, sigmoid, None, groups, top)
+        b, _ = _check(l, k, sigmoid, zero, groups, top)
+        assert np.array_equal(a, b)
+    assert a[0, 0] == 0 and a[3, 0] == 16
+
+
 def test_small_logits_that_fp64_does_tell_apart():
     # steps of 2^-46: scores 1.4e-14 apart, some sixty fp64 steps
     l = np.full((2, 32), -1.0, np.float32)
