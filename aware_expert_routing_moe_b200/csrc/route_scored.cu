@@ -124,14 +124,16 @@ __device__ __forceinline__ double reciprocal(double y) {
     r = fma(r, fma(-y, r, 1.0), r);
     return fma(r, fma(-y, r, 1.0), r);
 }
+// Scores below exp(-700), 1e-304, are 0 (both kinds).
 __device__ __forceinline__ double sigmoid(float l) {
     const double z = exp_neg(static_cast<double>(fmaxf(-fabsf(l), -700.0f)));
     const double r = reciprocal(1.0 + z);
-    return l >= 0.0f ? r : z * r;
+    return l >= 0.0f ? r : l >= -700.0f ? z * r : 0.0;
 }
-// exp(l - top); exp(-700) below
+// exp(l - top)
 __device__ __forceinline__ double exp_from(float l, float top) {
-    return exp_neg(fmax(static_cast<double>(l) - static_cast<double>(top), -700.0));
+    const double x = static_cast<double>(l) - static_cast<double>(top);
+    return x >= -700.0 ? exp_neg(x) : 0.0;
 }
 __device__ __forceinline__ int round_int(double v) { return __double2loint(v + ROUND); }
 
@@ -382,7 +384,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int b, const int (&gr
     double s = 0.0;
     if (mine >= 0) {
         const float v = clean_logit(__ldg(logits + mine));
-        s = sig ? (v >= -700.0f ? sigmoid(v) : 0.0) : exp_from(v, shift);
+        s = sig ? sigmoid(v) : exp_from(v, shift);
     }
     const double sum = a.rule.renorm ? warp_sum(s) : z;
     if (lane < a.k) {

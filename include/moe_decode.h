@@ -354,7 +354,9 @@ size_t moe_route_workspace_bytes(moe_dims_t dims);
  * counts as the largest finite value; a token with fewer than k experts to
  * choose from gets -1 and weight 0 in the slots left (a token with none is
  * in no list: padding).  bias must be finite.  The choice follows the exact
- * values of c as far as fp64 tells them apart, not their fp32 roundings.
+ * values of c as far as fp64 tells them apart, not their fp32 roundings;
+ * scores below 1e-304 count as 0 (a token that is steered to such experts
+ * only has weights of 0).
  * Deterministic.  ws: moe_route_workspace_bytes(dims) bytes, 256-byte
  * aligned, zero-filled once before its first use. */
 moe_status_t moe_route_scored(const float *logits, const float *bias, moe_dims_t dims, moe_scoring_t rule,

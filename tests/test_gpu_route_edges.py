@@ -84,6 +84,21 @@ def test_small_logits_that_fp64_does_tell_apart():
         _check(l, 4, sigmoid, np.zeros(32, np.float32))
 
 
+def test_scores_below_fp64_count_as_zero():
+    # the bias steers to experts whose softmax scores are below the smallest
+    # fp64 number: their weights are zero, as with sigmoid scores
+    l = np.array([[0.0, -800.0, -900.0, np.finfo(np.float32).min] + [-1000.0] * 12], np.float32)
+    bias = np.array([-2.0, 1.0, 0.5, 0.25] + [0.0] * 12, np.float32)
+    for renorm in (True, False):
+        sel, w = _check(l, 3, False, bias, renorm=renorm)
+        assert sel.tolist() == [[1, 2, 3]] and np.all(w == 0)
+    sel, w = _check(np.where(l == 0, -2000, l).astype(np.float32), 3, True, bias)
+    assert sel.tolist() == [[1, 2, 3]] and np.all(w == 0)
+    # one of the chosen holds all of the weight
+    _, w = _check(l, 3, False, np.array([0.0, 1.5, 0.5] + [-1.0] * 13, np.float32), scale=2.5)
+    assert w.tolist() == [[0.0, 2.5, 0.0]]
+
+
 @pytest.mark.parametrize("E,k", [(1, 1), (33, 4), (160, 6), (512, 16)])
 @pytest.mark.parametrize("B", [16, 17, 512, 513, 1100])
 @pytest.mark.parametrize("masked", [False, True])
