@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict
     if (threadIdx.x == 0) scale[tile] = pow2(e);
 }
 
-// One block per token.
-__global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ yp, const float *__restrict__ w,
-                                                      const int32_t *__restrict__ cnt,
-                                                      const int32_t *__restrict__ inv, int d, int k,
-                                                      void *__restrict__ y, int y_bf16) {
+// One block per token.  yp, cnt and inv are the kernel's before, which may
+// still run when this one starts: no load of theirs may be taken for one of
+// unchanging memory and move in front of the wait.
+__global__ void __launch_bounds__(256) combine_kernel(const float *yp, const float *w, const int32_t *cnt,
+                                                      const int32_t *inv, int d, int k, void *y, int y_bf16) {
     __shared__ int s_p[K_MAX];
     __shared__ float s_w[K_MAX];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *__restrict__ 
     for (int c = threadIdx.x * 4; c < d; c += blockDim.x * 4) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < n; ++j) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(yp + static_cast<size_t>(s_p[j]) * d + c));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(yp + static_cast<size_t>(s_p[j]) * d + c));
             s.x = fmaf(s_w[j], v.x, s.x);
             s.y = fmaf(s_w[j], v.y, s.y);
             s.z = fmaf(s_w[j], v.z, s.z);
