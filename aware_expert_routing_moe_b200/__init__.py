@@ -405,10 +405,15 @@ def _buf(t, n: int, types, dev: int):
 
 
 def _weight(w, scale, E: int, rows: int, cols: int, dev: int):
-    """Addresses of e4m3 matrices [E][rows][cols] and their block scales."""
+    """Addresses of e4m3 matrices [E][rows][cols] and their block scales
+    (of that shape, or flat)."""
+    rb, cb = (rows + 127) // 128, (cols + 127) // 128
+    if (w.dtype in _E4M3 and w.numel() == E * rows * cols and w.size(-1) == cols and w.get_device() == dev
+            and w.is_contiguous() and scale.dtype in _F32 and scale.numel() >= E * rb * cb
+            and (scale.size(-1) == cb or scale.ndim != 3) and scale.get_device() == dev and scale.is_contiguous()):
+        return w.data_ptr(), scale.data_ptr()
     if w.shape != (E, rows, cols):
         raise ValueError(f"weights of shape {tuple(w.shape)} where the call's sizes need {(E, rows, cols)}")
-    rb, cb = -(-rows // 128), -(-cols // 128)
     if scale.ndim == 3 and scale.shape != (E, rb, cb):
         raise ValueError(f"weight scales of shape {tuple(scale.shape)} where the call's sizes need {(E, rb, cb)}")
     return _buf(w, E * rows * cols, _E4M3, dev), _buf(scale, E * rb * cb, _F32, dev)
