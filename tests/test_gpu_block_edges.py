@@ -24,6 +24,14 @@ def _lib():
 
 # ---------------------------------------------------------- quantisation --
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(2047, 144), (2048, 16), (2049, 1040), (2500, 2064), (2048, 4112)])
+def test_quantize_many_rows(dtype, rows, cols):
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(3 * torch.randn(rows, 1, generator=g))
+    _check_quantized(x.to(dtype).cuda(), 1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,cols,block_rows", [(7, 400, 1), (2100, 1040, 1), (300, 272, 128)])
 def test_infinities_and_nan_become_nan(dtype, rows, cols, block_rows):
     # and the finite values of their blocks are rounded as if they were zeros
@@ -92,6 +100,70 @@ def test_ffn_whose_h_overflows_is_nan(B, d, E, k, F, dtype):
     y = moe.moe_expert_ffn_blocks(dirty, *args, dev, k)
     other = torch.arange(B, device="cuda") != 5
     assert torch.isnan(y[5]).all() and torch.equal(y[other], clean[other])
+
+
+@pytest.mark.parametrize("x_dtype,y_dtype", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("B,d,E,k,F", [(1, 256, 4, 2, 128), (17, 512, 8, 4, 256), (260, 272, 2, 2, 144), (3, 16, 2, 1, 16)])
+def test_ffn_of_one_type_into_the_other(B, d, E, k, F, x_dtype, y_dtype):
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, x_dtype)
+    y = moe.moe_expert_ffn_blocks(x, *args, dev, k, y_dtype=y_dtype)
+    assert y.dtype == y_dtype
+    _check_ffn(y, x, L, vals)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ffn_of_a_long_padded_batch(dtype):
+    # rows copied to their entries by the wide quantisation, some skipped
+    L, dev, x, args, vals = _ffn_setup(900, 272, 6, 3, 144, dtype, empty=0.2)
+    assert L["offsets"][-1] < 2700
+    ws = moe.new_blocks_workspace(900, 272, 6, 3, 144)
+    y = moe.moe_expert_ffn_blocks(x, *args, dev, 3, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, vals)
+
+
+@pytest.mark.parametrize("B,mode,kw", [(8, moe.MOE_RESELECT_OEA, dict(k0=2)), (64, moe.MOE_RESELECT_XSHARE, dict(budget=8)),
+                                       (128, moe.MOE_RESELECT_XSHARE, dict(budget=6)),
+                                       (128, moe.MOE_RESELECT_XSHARE_HIER, dict(budget=16, group=4)),
+                                       (100, moe.MOE_RESELECT_AFFINITY, {}), (256, moe.MOE_RESELECT_NONE, {})])
+def test_lists_of_the_reselection_rules(B, mode, kw):
+    d, E, k, F = 256, 64, 4, 128
+    rng = np.random.default_rng([21, B])
+    x = torch.from_numpy(rng.standard_normal((B, d)).astype(np.float32)).cuda()
+    Wg = torch.from_numpy((rng.standard_normal((E, d)) * 0.1).astype(np.float32)).cuda()
+    logits, probs, _, _ = moe.moe_route(x, Wg, None, k)
+    _, _, dev = moe.moe_reselect(logits, probs, k, mode, **kw)
+    L = {n: v.cpu().numpy() for n, v in dev.items()}
+    L["n_active"] = int(L["n_active"][0])
+    mats = [_weights(rng, E, F, d), _weights(rng, E, F, d), _weights(rng, E, d, F)]
+    ws = moe.new_blocks_workspace(B, d, E, k, F)
+    y = moe.moe_expert_ffn_blocks(x, *[t for m in mats for t in m[:2]], dev, k, ws=ws)
+    assert moe.moe_check_error(ws) == 0
+    _check_ffn(y, x, L, [m[2] for m in mats])
+
+
+# --------------------------------------------------------- damaged lists --
+@pytest.mark.parametrize("B,d,E,k,F", SIZES[:2])
+@pytest.mark.parametrize("field,value", [("n_active", -1), ("n_active", 99), ("n_active", 2 ** 31 - 1), ("active", 6),
+                                         ("active", -2), ("active", -2 ** 31), ("offsets", 10 ** 6), ("offsets", -3),
+                                         ("tok", 150), ("tok", -1), ("tok", 2 ** 31 - 1), ("tok", -2 ** 31)])
+def test_damaged_lists_touch_nothing_else(B, d, E, k, F, field, value):
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+    dev = {n: v.clone() for n, v in dev.items()}
+    dev[field][1 if field == "offsets" else 0] = value
+    ws, gws = moe.new_blocks_workspace(B, d, E, k, F), moe.new_gemm_workspace()
+    guard = 16
+    buf = torch.full((B + 2 * guard, d), 3.0, dtype=BF16, device="cuda")
+    moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws, y=buf[guard:guard + B])
+    assert moe.moe_check_error(ws) == 6
+    assert torch.all(buf[:guard] == 3) and torch.all(buf[guard + B:] == 3)
+    gbuf = torch.full((B * k + 2 * guard, F), 5.0, dtype=BF16, device="cuda")
+    q, s = moe.moe_quantize_blocks(x)
+    moe.moe_expert_gemm_blocks(q, s, args[0], args[1], dev, k, ws=gws, y=gbuf[guard:guard + B * k])
+    assert moe.moe_check_error(gws) == 6
+    assert torch.all(gbuf[:guard] == 5) and torch.all(gbuf[guard + B * k:] == 5)
+    if field != "tok":  # runs as an empty call
+        assert torch.all(buf[guard:guard + B] == 0) and torch.all(gbuf == 5)
 
 
 # ------------------------------------------- streams, workspaces, limits --
