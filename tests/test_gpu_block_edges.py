@@ -270,3 +270,69 @@ def test_a_tile_counter_below_zero_is_reported(B, d, E, k, F):
     y = moe.moe_expert_ffn_blocks(x, *args, dev, k, ws=ws)
     assert moe.moe_check_error(ws) == 0
     _check_ffn(y, x, L, vals)
+
+
+@pytest.mark.parametrize("B", [12, 300])
+def test_calls_captured_without_a_workspace(B):
+    # the graph holds the workspaces and their zero-fills
+    d, E, k, F = 256, 8, 2, 128
+    L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+    logits = torch.from_numpy(np.random.default_rng(B).standard_normal((B, E)).astype(np.float32)).cuda()
+
+    def chain():
+        sel, w, lists = moe.moe_route_scored(logits, k)
+        q, s = moe.moe_quantize_blocks(x)
+        return sel, w, moe.moe_expert_gemm_blocks(q, s, args[0], args[1], lists, k), moe.moe_expert_ffn_blocks(x, *args, lists, k)
+
+    want = [t.clone() for t in chain()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_the_default_stream_by_its_handle():
+    L, dev, x, args, vals = _ffn_setup(150, 256, 4, 3, 256, BF16)
+    want = moe.moe_expert_ffn_blocks(x, *args, dev, 3)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # the call runs on the default stream all the same
+        y = moe.moe_expert_ffn_blocks(x, *args, dev, 3, stream=0)
+        litter = _litter()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_activations_may_be_overwritten_by_the_result():
+    for B, d, E, k, F in SIZES:
+        L, dev, x, args, vals = _ffn_setup(B, d, E, k, F, BF16)
+        want = moe.moe_expert_ffn_blocks(x, *args, dev, k)
+        assert torch.equal(moe.moe_expert_ffn_blocks(x, *args, dev, k, y=x), want)
+
+
+@pytest.mark.parametrize("B", [5, 200])  # tiles of 16 and of 128 entries
+def test_product_of_the_largest_matrix(B):
+    d = F = 16384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.randint(0, 256, (1, F, d), device="cuda", dtype=torch.uint8, generator=g)
+    W = torch.where((W & 0x7F) == 0x7F, torch.full_like(W, 0x30), W)
+    S = torch.rand(1, F // 128, d // 128, device="cuda", generator=g) * 0.02 + 0.01
+    q, s = moe.moe_quantize_blocks(torch.randn(B, d, device="cuda", generator=g))
+    lists = {"n_active": _cuda(np.array([1, 0, 0, 0], np.int32)), "active": _cuda(np.zeros(1, np.int32)),
+             "offsets": _cuda(np.array([0, B], np.int32)), "tok": _cuda(np.arange(B, dtype=np.int32)),
+             "w": torch.ones(B, device="cuda")}
+    y = moe.moe_expert_gemm_blocks(q, s, W, S, lists, 1, y_dtype=F32)
+    x = _values(q) * bc.spread(s.cpu().numpy().astype(np.float64), B, d, 1)
+    rows = np.unique(np.r_[0, 127, 128, 255, 256, F - 257, F - 128, F - 1, np.random.default_rng(2).integers(0, F, 40)])
+    at = torch.from_numpy(rows).cuda()
+    w = bc.e4m3_decode(W[0][at].cpu().numpy()) * np.repeat(S[0][at // 128].cpu().numpy().astype(np.float64), 128, 1)
+    ref = x @ w.T
+    got = y[:, at].double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= bc.sum_bound(d, np.abs(x) @ np.abs(w).T) + bc.HALF_STEP["f32"] * np.abs(ref))

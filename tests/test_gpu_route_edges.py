@@ -148,3 +148,46 @@ def test_two_launches_captured_and_replayed():
         ref = bc.lists_of(rsel, out[1].cpu().numpy(), E)
         for n in ("active", "offsets", "tok"):
             assert np.array_equal(lists[n].cpu().numpy(), ref[n]), n
+
+
+def test_the_largest_batch():
+    # 65536 tokens, 512 experts, 16 of them, some tokens masked: the choice is
+    # the order of the logits (distinct, no bias), lists by a stable sort
+    B, E, k = 65536, 512, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    l = torch.rand(B, E, device="cuda", generator=g).argsort(1).float() * 0.01
+    l[::97] = -float("inf")
+    sel, w, lists = moe.moe_route_scored(l, k, moe.MOE_SCORE_SIGMOID, scale=2.0)
+    val, idx = l.sort(1, descending=True)
+    want = torch.where(val[:, :k] > -float("inf"), idx[:, :k], torch.full_like(idx[:, :k], -1))
+    assert torch.equal(sel.long(), want)
+    s = torch.sigmoid(val[:, :k].double())
+    rw = torch.nan_to_num(s / s.sum(1, keepdim=True) * 2.0)
+    assert torch.all((w.double() - rw).abs() <= W_TOL * rw)
+    flat = torch.where(want < 0, E, want).reshape(-1)
+    order = flat.argsort(stable=True)
+    n = int((flat < E).sum())
+    counts = torch.bincount(flat, minlength=E + 1)[:E]
+    assert int(lists["n_active"][0]) == E and torch.all(counts > 0)
+    assert torch.equal(lists["active"].long(), torch.arange(E, device="cuda"))
+    assert torch.equal(lists["offsets"][1:].long(), counts.cumsum(0)) and int(lists["offsets"][0]) == 0
+    assert torch.equal(lists["tok"][:n].long(), order[:n] // k) and torch.all(lists["tok"][n:] == -1)
+    assert torch.equal(lists["w"][:n], w.reshape(-1)[order[:n]]) and torch.all(lists["w"][n:] == 0)
+
+
+@pytest.mark.parametrize("B", [100, 700])
+def test_two_streams_at_once(B):
+    ls = [torch.from_numpy(_logits(B, E, 20)).cuda() for E in (64, 256)]
+    want = [moe.moe_route_scored(l, 8) for l in ls]
+    state = [((torch.empty_like(s), torch.empty_like(w)), moe.alloc_lists(B, l.shape[1], 8),
+              moe.new_route_workspace(B, l.shape[1], 8)) for l, (s, w, _) in zip(ls, want)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for l, (out, lists, ws), st in zip(ls, state, streams):
+            moe.moe_route_scored(l, 8, out=out, lists=lists, ws=ws, stream=st)
+    torch.cuda.synchronize()
+    for (out, lists, ws), (s, w, ref) in zip(state, want):
+        assert torch.equal(out[0], s) and torch.equal(out[1], w)
+        for n in ("active", "offsets", "tok", "w"):
+            assert torch.equal(lists[n], ref[n]), n
