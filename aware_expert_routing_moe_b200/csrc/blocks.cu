@@ -36,13 +36,13 @@
 // error, lets its copies and MMAs land and leaves.
 //
 // What bounds it, measured.  Few entries: HBM.  Expert FFN, Qwen3-30B shape,
-// 16 tokens: 64 us for 321 MB (58 of it this kernel, 312 MB read, tensor
-// pipe 4 % busy); 1 token 26 us, of which the chain of latencies (claim,
-// first copies, gate/up, publication, down, combine) is about 20; Qwen3-235B
-// shape, 8 tokens: 135 us, 6.3 TB/s.  Many entries: the copies from L2 and
-// the additions.  A stage of 48 KB takes about 970 cycles to arrive, its four
-// MMAs 512, the additions 500 to 1100: product 2000 x 4096 x 4096 51 us (1.32
-// PFLOP/s), expert FFN with 4096 tokens 380 us.  Pairs of CTAs
+// 16 tokens: 62 us for 321 MB (58 of it this kernel, 312 MB read, 5.4 TB/s,
+// tensor pipe 4 % busy); 1 token 25 us, of which the chain of latencies
+// (claim, first copies, gate/up, publication, down, combine) is about 20;
+// Qwen3-235B shape, 8 tokens: 134 us, 6.3 TB/s.  Many entries: the copies from
+// L2 and the additions.  A stage of 48 KB takes about 970 cycles to arrive,
+// its four MMAs 512, the additions 500 to 1100: product 2000 x 4096 x 4096
+// 52 us (1.29 PFLOP/s), expert FFN with 4096 tokens 376 us.  Pairs of CTAs
 // (cta_group::2), which halve the weight copies, were no faster: then the
 // sub-partition that issues the MMAs falls behind with its additions.
 #include <cuda_bf16.h>

@@ -12,8 +12,9 @@
 // the result is fixed bit by bit, whatever computes it.
 //
 // Bound by HBM: each value is read once and a byte written.  Measured: 4096
-// x 2048 bf16 rows 5.1 us (25.4 MB, 5.0 TB/s); 128 matrices of 768 x 2048
-// bf16 103 us (604 MB, 5.9 TB/s, 89 % of the measured copy rate).
+// x 2048 bf16 rows 6.4 us with inputs from HBM (25.4 MB, 4.0 TB/s: a short
+// launch), 4.9 us where they stay in L2; 128 matrices of 768 x 2048 bf16 89 us
+// (604 MB, 6.8 TB/s, 1.04 of the measured copy rate).
 #include <cuda_bf16.h>
 
 #include "blocks.h"
@@ -24,7 +25,9 @@ namespace {
 constexpr unsigned ALL = 0xffffffffu;
 constexpr unsigned INF_BITS = 0x7f800000u;  // magnitude bits of fp32 infinity; NaN above
 // Rows from which a warp takes 2048 (bf16) or 1024 (fp32) columns instead of
-// 512 (4096 x 2048 bf16: 4.65 against 4.99 us).
+// 512 (2048 columns, bf16: 2048 rows 4.3 against 4.1 us, 4096 rows 6.5 and
+// 6.5, 8192 rows 9.5 against 11.2; fp32: 5.5 against 5.4, 7.9 against 8.1,
+// 13.7 against 14.8).
 constexpr long long WIDE_ROWS = 2048;
 
 // Exponent e of the scale 2^e for a block whose largest magnitude is top

@@ -15,16 +15,20 @@
 // reciprocal (about 25 operations an expert); the warp then ranks 28-bit
 // images of the values, which one warp reduction each finds the largest of,
 // and ranks the fp64 values themselves only for a token in which two
-// neighbours of the order it uses are too close for that (about one in 10^4
-// random tokens, and every exact tie).  Without a bias, and with groups
-// valued by their best expert, the logits rank (a score is monotone in its
-// logit) and no score but the chosen ones is computed.
+// neighbours of the order it uses are too close for that: about one random
+// token in 10^4 with fp32 logits, and every exact tie, which logits of bf16
+// precision have in 22 to 37 % of tokens (64 to 256 experts, k = 8).  Without
+// a bias, and with groups valued by their best expert, the logits rank (a
+// score is monotone in its logit) and no score but the chosen ones is
+// computed, except among logits so near 0 that fp64 scores are equal.
 //
-// Bound by instructions: about 1900 a token with 256 experts in 8 groups
-// (scores 460, groups 390, the k + 1 rounds 370).  Measured: 1 token 8.5 us,
-// 77 tokens 9.3 us, 8192 tokens 39 us (choice 25, lists 10).  With fp32
-// scores and fp64 only for close calls a long batch took as long: some token
-// of it always needed fp64, at the latency of the whole fp64 path.
+// Bound by instructions: 1970 a token with 256 experts in 8 groups, sigmoid
+// scores and a bias (1570 without the groups, 1110 where the logits rank).
+// Measured: 1 token 8.6 us, 77 tokens (128 experts) 8.9 us, 8192 tokens 40 us
+// (under ncu the choice 28, the lists 12.5).  Exact ties: 8192 tokens, 128
+// experts, softmax 27 us with bf16-valued logits, 20 with fp32 ones.  With
+// fp32 scores and fp64 only for close calls a long batch took as long: some
+// token of it always needed fp64, at the latency of the whole fp64 path.
 #include <cfloat>
 #include <cmath>
 

@@ -422,7 +422,8 @@ size_t moe_blocks_workspace_bytes(moe_dims_t dims);
  *   h = silu(Wgate[e] x_t) * (Wup[e] x_t);
  * x[B][d] and h are rounded to e4m3 in blocks of 128 columns as
  * moe_quantize_blocks does (the format's 8-bit operands), sums are fp32,
- * y[B][d] is rounded once.  x_type, y_type: moe_dtype_t.  y is overwritten
+ * y[B][d] is rounded once.  x_type, y_type: moe_dtype_t (y may be x's own
+ * buffer where they are equal).  y is overwritten
  * (0 for a token in no list).  A listed token with an infinity or NaN in x,
  * or whose h overflows fp32, gets a row of NaN; the others are not touched.
  * A token's entries are added in list order: the result does not depend on
