@@ -1089,6 +1089,12 @@ cudaError_t launch_ar(const ProductMaps &maps, const ProductArgs &a, cudaStream_
         if (err != cudaSuccess) return err;
         err = cudaFuncSetAttribute(product_kernel<AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<AR>());
         if (err != cudaSuccess) return err;
+        if (!Ring<AR>::FEW) {  // setmaxnreg.inc would wait for ever for more registers than the launch has
+            cudaFuncAttributes at;
+            err = cudaFuncGetAttributes(&at, product_kernel<AR>);
+            if (err != cudaSuccess) return err;
+            if (at.numRegs * THREADS < 256 * REGS_EPI + 128 * REGS_COPY) return cudaErrorInvalidConfiguration;
+        }
         sms[dev] = n;
     }
     cudaLaunchConfig_t cfg = {};
