@@ -336,3 +336,42 @@ def test_product_of_the_largest_matrix(B):
     ref = x @ w.T
     got = y[:, at].double().cpu().numpy()
     assert np.all(np.abs(got - ref) <= bc.sum_bound(d, np.abs(x) @ np.abs(w).T) + bc.HALF_STEP["f32"] * np.abs(ref))
+
+
+@pytest.mark.parametrize("B", [6, 40, 100])
+def test_one_workspace_serves_every_entry_point_in_any_order(B):
+    d, E, k, F = 256, 32, 4, 128
+    rng = np.random.default_rng([41, B])
+    t = lambda *n: torch.from_numpy((rng.standard_normal(n) * 0.05).astype(np.float32)).cuda()
+    x, Wg = t(B, d) * 20, t(E, d)
+    bf = [m.bfloat16().view(torch.int16) for m in (t(E, F, d), t(E, F, d), t(E, d, F))]
+    q8 = [u for m in (t(E, F, d), t(E, F, d), t(E, d, F)) for u in moe.moe_quantize_blocks(m, 128)]
+    logits, many = t(B, E) * 20, t(3000, E) * 20
+    lists = moe.moe_route_scored(logits, k)[2]
+    q, s = moe.moe_quantize_blocks(x)
+    xs = torch.zeros(3, B, d, device="cuda")
+
+    def stack(ws):
+        xs[0] = x
+        return moe.moe_decode_stack(xs, [(Wg, None, *bf)] * 2, k, moe.MOE_RESELECT_XSHARE, budget=12, ws=ws)[1].clone()
+
+    calls = {
+        "layer": lambda ws: moe.moe_layer_decode(x, Wg, None, *bf, k, moe.MOE_RESELECT_AFFINITY, ws=ws),
+        "stack": stack,
+        "ffn": lambda ws: moe.moe_expert_ffn(x, *bf, lists, k, ws),
+        "route": lambda ws: moe.moe_route_scored(many, k, ws=ws)[1],
+        "route_few": lambda ws: moe.moe_route_scored(logits, k, ws=ws)[1],
+        "gemm": lambda ws: moe.moe_expert_gemm_blocks(q, s, *q8[:2], lists, k, ws=ws),
+        "ffn8": lambda ws: moe.moe_expert_ffn_blocks(x, *q8, lists, k, ws=ws),
+    }
+    n = max(moe.moe_workspace_bytes(B, d, E, k, F), moe.new_route_workspace(3000, E, k).numel(),
+            moe.new_blocks_workspace(B, d, E, k, F).numel(), 4096)
+    want = {name: call(torch.zeros(n, dtype=torch.uint8, device="cuda")) for name, call in calls.items()}
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for name in [rng.permutation(list(calls)) for _ in range(12)]:
+        for c in name:
+            y = calls[c](ws)
+            assert moe.moe_check_error(ws) == 0, c
+            # the bf16 paths add with fp32 atomics, in any order: some tens of
+            # additions, 2^-24 each
+            assert float((y.float() - want[c].float()).norm() / want[c].float().norm()) < 1e-5, c
