@@ -148,8 +148,9 @@ __device__ __forceinline__ int round_int(double v) { return __double2loint(v + R
 // close calls among such logits are decided by the scores.
 constexpr float TOP_LOGIT = 16.0f, LOW_LOGIT = -600.0f, TINY_LOGIT = 1.0f / 65536.0f;
 // Images: 28 bits of value (1 to 2^27 + 1; a unit is 2^-26 to 2^-25 of the
-// bound on the values' magnitude) over 4 bits of slot.  Rounding moves a value by half a unit, so two
-// that are more than NEAR units apart are in order; sums of two, SUM_NEAR.
+// bound on the values' magnitude) over 4 bits of slot.  Rounding moves a value
+// by half a unit, so two that are more than NEAR units apart are in order;
+// sums of two, SUM_NEAR.
 constexpr int SLOT_BITS = 4, NEAR = 2, SUM_NEAR = 4;
 
 // Experts lane + 32 i, i < NI.
